@@ -65,6 +65,49 @@ class SchedBatch(ctypes.Structure):
 
 ABORT_DEADLINE, ABORT_POOL_FULL = 1, 2
 
+
+class KV(ctypes.Structure):
+    _fields_ = [("pool", _vp), ("n_pages", _c_i64), ("page_elems", _c_i32), ("dtype", _c_i32),
+                ("n_kv_heads", _c_i32), ("head_dim", _c_i32), ("tokens_per_page", _c_i32),
+                ("n_requests", _c_i32), ("max_blocks", _c_i32)]
+
+
+class KVStep(ctypes.Structure):
+    _fields_ = [("n_planes", _c_i32), ("append", _c_i32), ("pages", _vp), ("n_page_ids", _c_i64),
+                ("past_len", _vp), ("new_len", _vp), ("n_tokens", _c_i32), ("tables", _vp),
+                ("seq_len", _vp), ("q_offsets", _vp), ("token_request", _vp), ("position", _vp),
+                ("slots", _vp)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", _c_i32), ("scaling", _c_i32), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double)]
+
+
+class QKV(ctypes.Structure):
+    _fields_ = [("n_tokens", _c_i32), ("n_q_heads", _c_i32),
+                ("q", _vp), ("q_token_stride", _c_i64), ("q_head_stride", _c_i64),
+                ("k", _vp), ("k_token_stride", _c_i64), ("k_head_stride", _c_i64),
+                ("v", _vp), ("v_token_stride", _c_i64), ("v_head_stride", _c_i64),
+                ("q_out", _vp), ("out_token_stride", _c_i64), ("out_head_stride", _c_i64),
+                ("position", _vp), ("k_slots", _vp), ("v_slots", _vp), ("turns", _vp),
+                ("rotary_dim", _c_i32), ("interleaved", _c_i32), ("cos_sin_scale", ctypes.c_float),
+                ("norm", _c_i32), ("eps", ctypes.c_float), ("q_weight", _vp), ("k_weight", _vp)]
+
+
+class Attn(ctypes.Structure):
+    _fields_ = [("n_q_heads", _c_i32), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("window", _c_i32), ("slopes", _vp), ("prefix_len", _vp), ("k_table", _vp),
+                ("v_table", _vp), ("seq_len", _vp),
+                ("q", _vp), ("q_token_stride", _c_i64), ("q_head_stride", _c_i64),
+                ("out", _vp), ("out_token_stride", _c_i64), ("out_head_stride", _c_i64),
+                ("lse", _vp)]
+
+
+ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "bands": 3}
+KV_MAX_REQUESTS, KV_MAX_PLANES = 16384, 4096
+
 _lib = None
 
 
@@ -129,6 +172,12 @@ def load(path: str = LIB_PATH):
         "slora_sched_finish": ([P, _c_i64], I),
         "slora_sched_step": ([P, P], I),
         "slora_sched_request_pages": ([P, _c_i64, P, I, P], I),
+        "slora_kv_tables": ([P, P, P], I),
+        "slora_rope_turns": ([P, P], I),
+        "slora_kv_write": ([P, P, P], I),
+        "slora_attn_workspace_size": ([P, P, I, P], I),
+        "slora_attn_decode": ([P, P, P, _c_i64, P], I),
+        "slora_attn_prefill": ([P, P, P, I, P, _c_i64, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -495,8 +544,56 @@ def bind_apply(call: Call, x: int, y: int, ws: int, ws_bytes: int, stream: int,
     return run
 
 
+def rope_turns(rope: Rope) -> np.ndarray:
+    out = np.empty(max(rope.rotary_dim // 2, 1), np.float64)
+    _check(load().slora_rope_turns(ctypes.byref(rope), _p(out)), "rope_turns")
+    return out
+
+
+def attn_workspace_size(kv: KV, attn: Attn, n_tokens: int) -> int:
+    n = _c_i64()
+    _check(load().slora_attn_workspace_size(ctypes.byref(kv), ctypes.byref(attn), n_tokens,
+                                            ctypes.byref(n)), "attn_workspace_size")
+    return n.value
+
+
+def _bound(name: str, args, keep):
+    """A no-argument callable of one entry point, its arguments converted once (see
+    bind_apply); `keep` holds what the arguments point to."""
+    f = getattr(load(), "slora_" + name)
+
+    def run():
+        rc = f(*args)
+        if rc != OK:
+            _check(rc, name)
+
+    run.keep = keep
+    return run
+
+
+def bind_kv_tables(kv: KV, step: KVStep, stream: int):
+    return _bound("kv_tables", (ctypes.byref(kv), ctypes.byref(step), _vp(stream)), (kv, step))
+
+
+def bind_kv_write(kv: KV, qkv: QKV, stream: int):
+    return _bound("kv_write", (ctypes.byref(kv), ctypes.byref(qkv), _vp(stream)), (kv, qkv))
+
+
+def bind_attn_decode(kv: KV, attn: Attn, ws: int, ws_bytes: int, stream: int):
+    return _bound("attn_decode", (ctypes.byref(kv), ctypes.byref(attn), _vp(ws), _c_i64(ws_bytes),
+                                  _vp(stream)), (kv, attn))
+
+
+def bind_attn_prefill(kv: KV, attn: Attn, q_offsets: int, n_tokens: int, ws: int, ws_bytes: int,
+                      stream: int):
+    return _bound("attn_prefill", (ctypes.byref(kv), ctypes.byref(attn), _vp(q_offsets),
+                                   _c_i32(n_tokens), _vp(ws), _c_i64(ws_bytes), _vp(stream)),
+                  (kv, attn))
+
+
 KERNELS = ["mbgmv_shrink", "mbgmv_expand", "sgmv_shrink", "sgmv_expand", "mbgmv_fused", "gather",
-           "fetch", "sgmv_fused", "mixed_fused", "multi_fused"]
+           "fetch", "sgmv_fused", "mixed_fused", "multi_fused", "kv_tables", "kv_write", "attn_decode",
+           "attn_prefill"]
 
 
 def timing_enable(on: bool):

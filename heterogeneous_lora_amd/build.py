@@ -22,8 +22,9 @@ BUILD_DIR = os.path.join(ROOT, "_build", "slora")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 ARCH = "gfx950"
 
-HOST_SRCS = ["pool.cpp", "plan.cpp", "api.cpp", "sched.cpp"]
-DEVICE_SRCS = ["mbgmv.hip", "sgmv.hip", "fetch.hip", "noalloc.hip", "gather.hip"]
+HOST_SRCS = ["pool.cpp", "plan.cpp", "api.cpp", "sched.cpp", "kv.cpp"]
+DEVICE_SRCS = ["mbgmv.hip", "sgmv.hip", "fetch.hip", "noalloc.hip", "gather.hip",
+               "kv_tables.hip", "kv_write.hip", "attn_decode.hip", "attn_prefill.hip"]
 
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function",
           f"-I{INCLUDE}", f"-I{CSRC}", "-D__HIP_PLATFORM_AMD__=1"]

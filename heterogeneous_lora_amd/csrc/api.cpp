@@ -675,6 +675,11 @@ hipError_t timed_fetch(const FetchPage* pages, int64_t n, uint16_t* pool, int32_
   });
 }
 
+hipError_t timed_call(int kernel, hipStream_t s, const std::function<hipError_t(const LaunchEvents&)>& launch) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  return timed_launch(kernel, s, launch);
+}
+
 int apply_shared(const slora_lora* L, const slora_routing* R, const void* x, void* y, void* ws,
                  int64_t ws_bytes, void* stream) {
   return run(L, R, x, nullptr, nullptr, y, ws, ws_bytes, stream, kApply, true);

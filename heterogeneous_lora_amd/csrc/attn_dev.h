@@ -1,0 +1,135 @@
+// Device code shared by the attention kernels: which keys a row sees, where a key's
+// vector lies in the pool, the score, matrix instructions, lane exchanges.
+#pragma once
+
+#include "device_common.h"
+
+namespace slora {
+namespace dev {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// A vector of zeros and one of quiet NaN (as long as the largest head), where loads of
+// keys past the end, and through a page id outside the pool, are pointed: every load
+// issues unconditionally, and no place of the pool that holds no key of the row is read.
+struct alignas(16) AttnFill {
+  uint16_t zero[256];
+  uint16_t nan_f16[256];
+  uint16_t nan_bf16[256];
+};
+constexpr AttnFill make_attn_fill() {
+  AttnFill f{};
+  for (int i = 0; i < 256; ++i) {
+    f.zero[i] = 0;
+    f.nan_f16[i] = 0x7E00;
+    f.nan_bf16[i] = 0x7FC0;
+  }
+  return f;
+}
+__device__ AttnFill kAttnFill = make_attn_fill();
+
+template <int DT>
+__device__ __forceinline__ uint64_t fill_addr(bool zero) {
+  return (uint64_t)(zero ? kAttnFill.zero : DT == SLORA_F16 ? kAttnFill.nan_f16 : kAttnFill.nan_bf16);
+}
+
+// n / tpp for n < 2^31 (magic and shift from the host).
+__device__ __forceinline__ uint32_t div_tpp(const AttnArgs& a, uint32_t n) {
+  return a.tpp == 1 ? n : __umulhi(n, a.tpp_magic) >> a.tpp_shift;
+}
+
+// The keys the rows of one workgroup see, as one run of indices [0, count): below `pre`
+// the key of that number, from there on that number + gap (a window leaves a hole behind
+// the prefix).
+struct Keys {
+  int32_t count, pre, gap;
+  __device__ __forceinline__ int32_t key(int32_t i) const { return i < pre ? i : i + gap; }
+};
+
+// For rows at positions p_min .. p_max of request r with n cached keys (p_max < n).
+__device__ __forceinline__ Keys keys_of(const AttnArgs& a, int r, int32_t n, int32_t p_min, int32_t p_max) {
+  const int32_t prefix = a.prefix ? min(max(a.prefix[r], 0), n) : 0;
+  const int32_t lo = a.window ? max(p_min - a.window + 1, 0) : 0;
+  const int32_t end = max(p_max + 1, prefix);
+  Keys k;
+  k.pre = min(prefix, lo);
+  k.gap = lo - k.pre;
+  if (lo >= end) {  // nothing past the prefix
+    k.gap = 0;
+    k.count = prefix;
+  } else {
+    k.count = end - k.gap;
+  }
+  return k;
+}
+
+// Whether the row at position p sees key j (j < n); prefix as above.
+__device__ __forceinline__ bool sees(const AttnArgs& a, int32_t prefix, int32_t p, int32_t j) {
+  return (j <= p && (a.window == 0 || p - j < a.window)) || j < prefix;
+}
+
+// Address of the first element of key j's vector (head h), given its page id.
+template <int DT>
+__device__ __forceinline__ uint64_t key_addr(const AttnArgs& a, int32_t page, int32_t j, int32_t h_off) {
+  const uint32_t in = a.tpp == 1 ? 0u : (uint32_t)j - div_tpp(a, (uint32_t)j) * (uint32_t)a.tpp;
+  const uint64_t at = (uint64_t)(a.pool + (int64_t)page * a.P + (uint32_t)(in * (uint32_t)a.row) + h_off);
+  return (uint32_t)page < a.n_pages_u ? at : fill_addr<DT>(false);
+}
+
+// Score in units of log 2 (weights are exp2 of differences).
+__device__ __forceinline__ float capped(const AttnArgs& a, float s) {
+  // cap tanh(x / cap) = cap - 2 cap / (exp(2 x / cap) + 1)
+  const float e = __builtin_amdgcn_exp2f(s * a.cap_in);
+  return a.cap_out - 2.0f * a.cap_out * __builtin_amdgcn_rcpf(e + 1.0f);
+}
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16x16(const uint4& x, const uint4& y, f32x4 c) {
+  if constexpr (DT == SLORA_F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
+}
+template <int DT>
+__device__ __forceinline__ f32x16 mfma32x32(const uint4& x, const uint4& y, f32x16 c) {
+  if constexpr (DT == SLORA_F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
+}
+
+// Lane l with lane l ^ 32 (and l ^ 16).
+__device__ __forceinline__ float max32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float sum16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Halves of dwords a and b at the same place: (a.lo, b.lo) or (a.hi, b.hi).
+__device__ __forceinline__ uint32_t pair_lo(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+// exp2(m_part - m) as a weight of a partial result: 0 for a part that saw nothing.
+__device__ __forceinline__ float part_weight(float m_part, float m) {
+  return m_part == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m_part - m);
+}
+
+}  // namespace dev
+}  // namespace slora

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <functional>
 #include <string>
 #include <vector>
 
@@ -249,5 +250,49 @@ hipError_t launch_fetch(const FetchPage* pages, int64_t n, uint16_t* pool, int32
 // launch_fetch, timed as SLORA_K_FETCH while kernel timing is on (api.cpp).
 hipError_t timed_fetch(const FetchPage* pages, int64_t n, uint16_t* pool, int32_t page_elems,
                        hipStream_t s);
+
+// ---------------------------------------------------------------- KV cache and attention
+// Threads of one launch must stay below this.
+constexpr int64_t kMaxThreads = int64_t(1) << 32;
+// One attention call as the kernels see it (checked by kv.cpp). Strides in elements.
+struct AttnArgs {
+  const uint16_t* pool;
+  uint32_t n_pages_u;       // page ids below it are in the pool (as unsigned: -1 is not)
+  int32_t P, tpp;
+  uint32_t tpp_magic, tpp_shift;  // n / tpp = umulhi(n, magic) >> shift for n < 2^31, tpp > 1
+  int32_t row;              // n_kv_heads * head_dim
+  int32_t n_req, max_blocks, hk, group, D;
+  int32_t max_len;          // max_blocks * tpp
+  const int32_t *kt, *vt, *seq, *prefix;
+  const uint16_t* q;
+  int64_t q_ts, q_hs;
+  uint16_t* out;
+  int64_t o_ts, o_hs;
+  float* lse;
+  float scale2;             // scale * log2(e)
+  float cap_in, cap_out;    // softcap > 0: 2 log2(e) scale / softcap, softcap log2(e); else 0
+  int32_t window;
+  const float* slopes;
+  // prefill
+  const int32_t* q_offsets;
+  int32_t n_tok;
+  // decode and prefill, rows split over the keys: partial results
+  float* part;
+  int32_t target;           // decode: workgroups to aim for
+};
+// Floats of one row's partial result: max, sum, and the head's dimensions.
+inline int64_t attn_part_floats(int32_t D) { return D + 2; }
+// Chunks of the cached keys a decode call is cut into, at most (all requests together),
+// given KV heads x 16-row groups of query heads.
+constexpr int32_t kDecodeTarget = 1024;
+inline int64_t decode_max_chunks(int32_t n_req, int32_t units) {
+  return (int64_t)n_req + (kDecodeTarget + units - 1) / units;
+}
+hipError_t launch_attn_decode(const AttnArgs& a, int32_t dtype, hipStream_t s, const LaunchEvents& ev);
+hipError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, hipStream_t s, const LaunchEvents& ev);
+hipError_t launch_kv_tables(const slora_kv& kv, const slora_kv_step& st, hipStream_t s, const LaunchEvents& ev);
+hipError_t launch_kv_write(const slora_kv& kv, const slora_qkv& w, hipStream_t s, const LaunchEvents& ev);
+// One call's launches, timed as kernel id `kernel` while kernel timing is on (api.cpp).
+hipError_t timed_call(int kernel, hipStream_t s, const std::function<hipError_t(const LaunchEvents&)>& launch);
 
 }  // namespace slora

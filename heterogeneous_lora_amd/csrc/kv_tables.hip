@@ -1,0 +1,202 @@
+// Block tables, slot maps and positions of a step, built on the GPU from its requests'
+// lengths (slora_kv_tables): the S-LoRA overview, section "1. Unified Paging", keeps the
+// KV cache on pages of the unified pool; a request's tokens are found through a table of
+// its pages.
+//
+// The page list comes block by block, each block's planes together; a table row holds one
+// plane's blocks. So the work is a transposition, bound by the bytes of the list and the
+// tables: a workgroup reads a run of blocks (their ids of up to 64 planes lie together in
+// the list), turns it in LDS and writes each plane's part of the row. Where a request's
+// blocks start in the list and its tokens in the step's arrays is the sum of the lengths
+// before it: every workgroup adds them up by itself (at most 16384 of them, L2 hits),
+// which takes less time than another launch and a hand-over through memory.
+#include "device_common.h"
+
+namespace slora {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPlanes = 64;       // planes a workgroup turns at once
+constexpr int kTileInts = 4096;   // page ids of one LDS tile
+constexpr int kTileBlocks = 1024; // blocks of one tile at most
+// Rows are padded to an odd stride against bank conflicts; tile_blocks() keeps every
+// (blocks x odd stride) within this.
+constexpr int kLdsInts = 5120;
+
+// Blocks of a tile for `planes` planes: a multiple of 64 when it is not one wave's worth.
+__device__ __forceinline__ int tile_blocks(int planes) {
+  const int n = kTileInts / planes & ~63;
+  return n > kTileBlocks ? kTileBlocks : n < 64 ? 64 : n;
+}
+static_assert(1024 * (4 | 1) <= kLdsInts && 64 * (64 | 1) <= kLdsInts && 640 * (6 | 1) <= kLdsInts,
+              "LDS tile");
+
+struct Sums {
+  int64_t blocks, tokens;
+};
+
+__device__ __forceinline__ int64_t div_up(int64_t a, int32_t b) {
+  const uint64_t n = (uint64_t)a + (uint32_t)b - 1;
+  return (n >> 32) ? (int64_t)(n / (uint32_t)b) : (int64_t)((uint32_t)n / (uint32_t)b);
+}
+
+struct Request {
+  int64_t past, seq;      // tokens cached before, and after the step
+  int64_t first, blocks;  // its blocks [first, blocks) are in the list
+};
+
+__device__ __forceinline__ Request request(const slora_kv_step& st, int32_t tpp, int r) {
+  Request q;
+  q.past = max(st.past_len[r], 0);
+  q.seq = q.past + max(st.new_len[r], 0);
+  q.blocks = div_up(q.seq, tpp);
+  q.first = st.append ? div_up(q.past, tpp) : 0;
+  return q;
+}
+
+// Sums over requests [0, r) of their list blocks and new tokens, on every thread.
+__device__ Sums sums_before(const slora_kv_step& st, int32_t tpp, int r) {
+  __shared__ Sums part[kThreads / 64];
+  Sums s{0, 0};
+  for (int i = (int)threadIdx.x; i < r; i += kThreads) {
+    const Request q = request(st, tpp, i);
+    s.blocks += q.blocks - q.first;
+    s.tokens += q.seq - q.past;
+  }
+  for (int d = 32; d; d >>= 1) {
+    s.blocks += __shfl_xor(s.blocks, d);
+    s.tokens += __shfl_xor(s.tokens, d);
+  }
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = part[0];
+  for (int w = 1; w < kThreads / 64; ++w) {
+    s.blocks += part[w].blocks;
+    s.tokens += part[w].tokens;
+  }
+  return s;
+}
+
+// blockIdx.y = request (n_requests: the rows past the step's tokens), blockIdx.x = its
+// share of the row's tiles, blockIdx.z = group of kPlanes planes.
+__global__ __launch_bounds__(kThreads) void kv_tables_kernel(slora_kv_step st, int64_t n_pages,
+                                                             int32_t tpp, int32_t n_req,
+                                                             int32_t max_blocks) {
+  __shared__ int32_t tile[kLdsInts];
+  const int r = (int)blockIdx.y, tid = (int)threadIdx.x;
+  const int p0 = (int)blockIdx.z * kPlanes, np = min(st.n_planes - p0, kPlanes);
+  const int64_t T = st.n_tokens;
+  const int sub = (int)blockIdx.x, n_sub = (int)gridDim.x;
+
+  if (r == n_req) {
+    const int64_t total = min(sums_before(st, tpp, n_req).tokens, T);
+    if (sub == 0 && p0 == 0 && tid == 0) st.q_offsets[n_req] = (int32_t)total;
+    for (int64_t t = total + sub * kThreads + tid; t < T; t += n_sub * kThreads) {
+      if (p0 == 0) {
+        st.token_request[t] = -1;
+        st.position[t] = -1;
+      }
+      for (int p = 0; p < np; ++p) st.slots[(int64_t)(p0 + p) * T + t] = -1;
+    }
+    return;
+  }
+
+  const Request q = request(st, tpp, r);
+  // blocks this row deals with: all of it, or the ones the new tokens touch
+  const int64_t b_begin = st.append ? q.past / tpp : 0;
+  const int64_t b_used = q.seq > q.past || !st.append ? min(q.blocks, (int64_t)max_blocks) : b_begin;
+  const int64_t b_end = st.append ? b_used : max_blocks;
+  const int tb = tile_blocks(np), stride = np | 1;
+  const int64_t tile0 = b_begin + (int64_t)sub * tb;
+  if (sub != 0 && tile0 >= b_end) return;
+
+  // Rows past the request's blocks are -1 and need no sums.
+  const bool any_used = sub == 0 || tile0 < b_used;
+  Sums before{0, 0};
+  if (any_used) before = sums_before(st, tpp, r);
+  const int64_t t_first = before.tokens;
+  if (sub == 0 && p0 == 0 && tid == 0) {
+    st.seq_len[r] = (int32_t)min(q.seq, (int64_t)INT32_MAX);
+    st.q_offsets[r] = (int32_t)min(t_first, T);
+  }
+
+  for (int64_t b0 = tile0; b0 < b_end; b0 += (int64_t)n_sub * tb) {
+    const int64_t b1 = min(b0 + tb, b_end);
+    const int n_used = (int)max(min(b1, b_used) - b0, (int64_t)0);
+    if (n_used > 0) {
+      __syncthreads();  // the previous tile has been read
+      for (int i = tid; i < n_used * np; i += kThreads) {
+        const int b = i / np, p = i - b * np;
+        const int64_t blk = b0 + b;
+        int32_t page = -1;
+        if (blk >= q.first) {
+          const int64_t at = (before.blocks + blk - q.first) * st.n_planes + p0 + p;
+          if (at < st.n_page_ids) page = st.pages[at];
+        } else {  // append: the block the step before left part full
+          page = st.tables[((int64_t)(p0 + p) * n_req + r) * max_blocks + blk];
+        }
+        tile[b * stride + p] = page;
+      }
+      __syncthreads();
+    }
+    // table rows: from the tile, -1 past the request's blocks
+    const int w0 = (int)max(q.first - b0, (int64_t)0);  // append: the part-full block stays
+    const int w1 = (int)(b1 - b0);
+    const int lanes = tb < kThreads ? 64 : kThreads;
+    for (int p = tid / lanes; p < np; p += kThreads / lanes) {
+      int32_t* row = st.tables + ((int64_t)(p0 + p) * n_req + r) * max_blocks + b0;
+      for (int b = w0 + tid % lanes; b < w1; b += lanes) row[b] = b < n_used ? tile[b * stride + p] : -1;
+    }
+    // slots, positions and ids of the new tokens on these blocks
+    const int64_t s0 = max(b0 * tpp, q.past), s1 = min((b0 + n_used) * (int64_t)tpp, q.seq);
+    const int64_t at = t_first + s0 - q.past;
+    const int n_tok = (int)max(min(s1 - s0, T - at), (int64_t)0);
+    for (int p = tid / lanes; p < np; p += kThreads / lanes) {
+      for (int i = tid % lanes; i < n_tok; i += lanes) {
+        const int64_t pos = s0 + i;
+        const int64_t blk = (uint32_t)pos / (uint32_t)tpp;  // pos < 2^32
+        const int32_t page = tile[(int)(blk - b0) * stride + p];
+        const bool ok = page >= 0 && page < n_pages;
+        st.slots[(int64_t)(p0 + p) * T + at + i] = ok ? (int64_t)page * tpp + (pos - blk * tpp) : -1;
+        if (p0 + p == 0) {
+          st.token_request[at + i] = r;
+          st.position[at + i] = (int32_t)min(pos, (int64_t)INT32_MAX);
+        }
+      }
+    }
+  }
+
+  // tokens past the table have no slot
+  const int64_t limit = (int64_t)max_blocks * tpp;
+  if (sub == 0 && q.seq > limit) {
+    const int64_t from = max(q.past, limit), at = t_first + from - q.past;
+    const int64_t n_tok = min(q.seq - from, T - at);
+    for (int64_t i = tid; i < n_tok; i += kThreads) {
+      if (p0 == 0) {
+        st.token_request[at + i] = r;
+        st.position[at + i] = (int32_t)min(from + i, (int64_t)INT32_MAX);
+      }
+      for (int p = 0; p < np; ++p) st.slots[(int64_t)(p0 + p) * T + at + i] = -1;
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_kv_tables(const slora_kv& kv, const slora_kv_step& st, hipStream_t s,
+                            const LaunchEvents& ev) {
+  const int groups = (st.n_planes + kPlanes - 1) / kPlanes;
+  // Shares of a row: enough workgroups to fill the device, no more than a row has tiles of
+  // 64 blocks (new tokens of one request alone, in append mode).
+  const int64_t rows = (int64_t)(kv.n_requests + 1) * groups;
+  int64_t sub = (2048 + rows - 1) / rows;
+  const int64_t tiles = ((int64_t)kv.max_blocks + 63) / 64;
+  if (sub > tiles) sub = tiles;
+  if (sub < 1) sub = 1;
+  hipExtLaunchKernelGGL(kv_tables_kernel, dim3((unsigned)sub, (unsigned)(kv.n_requests + 1), (unsigned)groups),
+                        dim3(kThreads), 0, s, ev.start, ev.stop, 0, st, kv.n_pages, kv.tokens_per_page,
+                        kv.n_requests, kv.max_blocks);
+  return hipGetLastError();
+}
+
+}  // namespace slora

@@ -277,3 +277,202 @@ class ServingLoop:
         self.sched.destroy()
         self.res.destroy()
         self.pool.destroy()
+
+
+TORCH_DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
+
+
+class Rope:
+    """Rotary positions: frequencies (slora_rope_turns) uploaded once, and the layout.
+
+    scaling: "none", "linear", "base" or "bands" (slora.h); cos_sin_scale multiplies the
+    cosines and sines (1 unless the model's scaling asks for another value)."""
+
+    def __init__(self, rotary_dim: int, theta: float = 10000.0, interleaved: bool = False,
+                 scaling: str = "none", factor: float = 1.0, original_len: float = 0.0,
+                 low_turns: float = 1.0, high_turns: float = 4.0, cos_sin_scale: float = 1.0,
+                 device: str = "cuda"):
+        self.rotary_dim, self.interleaved, self.cos_sin_scale = rotary_dim, interleaved, cos_sin_scale
+        self.turns_host = _lib.rope_turns(_lib.Rope(rotary_dim, _lib.ROPE_SCALING[scaling], theta, factor,
+                                                    original_len, low_turns, high_turns))
+        self.turns = torch.from_numpy(self.turns_host).to(device)
+
+
+class KVTables:
+    """Device arrays slora_kv_tables fills (slora.h, slora_kv_step). table: the tables of the
+    steps before, kept and extended by append calls (None: new ones, all -1)."""
+
+    def __init__(self, n_planes: int, n_requests: int, max_blocks: int, n_tokens: int,
+                 table: Optional[torch.Tensor] = None, device: str = "cuda"):
+        def ints(*shape, dtype=torch.int32):
+            return torch.full(shape, -1, dtype=dtype, device=device)
+        self.n_planes, self.n_requests, self.max_blocks = n_planes, n_requests, max_blocks
+        self.n_tokens = n_tokens
+        self.table = ints(n_planes, n_requests, max_blocks) if table is None else table
+        _expect("table", self.table, torch.int32, (n_planes, n_requests, max_blocks))
+        self.seq_len, self.q_offsets = ints(n_requests), ints(n_requests + 1)
+        self.token_request, self.position = ints(n_tokens), ints(n_tokens)
+        self.slots = ints(n_planes, n_tokens, dtype=torch.int64)
+
+
+def _expect(name: str, t: torch.Tensor, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+
+
+def _opt(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+class KVCache:
+    """The pool's KV pages as the attention operators see them (slora_kv).
+
+    Each bind_* method checks shapes and types, marshals one call's arguments once and
+    returns a no-argument callable; the method of the same name without bind_ makes the call
+    at once. Calls go to `stream` (the current stream at binding if None)."""
+
+    def __init__(self, pool: Optional[torch.Tensor], n_pages: int, page_elems: int = 0, dtype: str = "f16",
+                 n_kv_heads: int = 1, head_dim: int = 8, tokens_per_page: int = 1):
+        if pool is not None and pool.numel() * pool.element_size() < 2 * n_pages * page_elems:
+            raise ValueError(f"pool holds fewer than {n_pages} pages of {page_elems} elements")
+        self.pool, self.n_pages, self.page_elems, self.dtype = pool, n_pages, page_elems, dtype
+        self.n_kv_heads, self.head_dim, self.tokens_per_page = n_kv_heads, head_dim, tokens_per_page
+
+    def _kv(self, n_requests: int = 0, max_blocks: int = 0) -> _lib.KV:
+        return _lib.KV(_opt(self.pool), self.n_pages, self.page_elems, _lib.DTYPES[self.dtype],
+                       self.n_kv_heads, self.head_dim, self.tokens_per_page, n_requests, max_blocks)
+
+    def _rows(self, name: str, t: torch.Tensor, n: Optional[int] = None, heads: Optional[int] = None):
+        """A [rows, heads, head_dim] tensor of the cache's type with a dense last dimension."""
+        if t.dtype != TORCH_DTYPES[self.dtype] or t.dim() != 3 or t.shape[2] != self.head_dim or \
+                t.stride(2) != 1 or (n is not None and t.shape[0] != n) or \
+                (heads is not None and t.shape[1] != heads):
+            want = f"[{'rows' if n is None else n}, {'heads' if heads is None else heads}, {self.head_dim}]"
+            raise ValueError(f"{name}: expected {TORCH_DTYPES[self.dtype]} {want} with a dense last dimension, "
+                             f"got {t.dtype} {tuple(t.shape)}")
+        return t.data_ptr(), t.stride(0), t.stride(1)
+
+    @staticmethod
+    def _stream(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> int:
+        return (stream or torch.cuda.current_stream(t.device)).cuda_stream
+
+    # -- block tables, slots, positions (slora_kv_tables)
+    def bind_tables(self, tables: KVTables, pages: torch.Tensor, past_len: torch.Tensor,
+                    new_len: torch.Tensor, append: bool = False,
+                    stream: Optional[torch.cuda.Stream] = None):
+        t = tables
+        _expect("pages", pages, torch.int32, (pages.numel(),))
+        _expect("past_len", past_len, torch.int32, (t.n_requests,))
+        _expect("new_len", new_len, torch.int32, (t.n_requests,))
+        step = _lib.KVStep(t.n_planes, int(append), pages.data_ptr(), pages.numel(), past_len.data_ptr(),
+                           new_len.data_ptr(), t.n_tokens, t.table.data_ptr(), t.seq_len.data_ptr(),
+                           t.q_offsets.data_ptr(), t.token_request.data_ptr(), t.position.data_ptr(),
+                           t.slots.data_ptr())
+        call = _lib.bind_kv_tables(self._kv(t.n_requests, t.max_blocks), step, self._stream(t.table, stream))
+        call.tensors = (t, pages, past_len, new_len)
+        return call
+
+    def tables(self, *args, **kw):
+        self.bind_tables(*args, **kw)()
+
+    # -- norm, rotation, store (slora_kv_write)
+    def bind_write(self, q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor],
+                   q_out: torch.Tensor, position: torch.Tensor, k_slots: Optional[torch.Tensor],
+                   v_slots: Optional[torch.Tensor], rope: Optional[Rope] = None, norm: bool = False,
+                   q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                   eps: float = 1e-6, stream: Optional[torch.cuda.Stream] = None):
+        n, hq = q.shape[0], q.shape[1]
+        w = _lib.QKV()
+        w.n_tokens, w.n_q_heads = n, hq
+        w.q, w.q_token_stride, w.q_head_stride = self._rows("q", q)
+        w.q_out, w.out_token_stride, w.out_head_stride = self._rows("q_out", q_out, n, hq)
+        if k is not None and v is not None:
+            w.k, w.k_token_stride, w.k_head_stride = self._rows("k", k, n, self.n_kv_heads)
+            w.v, w.v_token_stride, w.v_head_stride = self._rows("v", v, n, self.n_kv_heads)
+            for name, s in (("k_slots", k_slots), ("v_slots", v_slots)):
+                _expect(name, s, torch.int64, (n,))
+            w.k_slots, w.v_slots = k_slots.data_ptr(), v_slots.data_ptr()
+        elif k is not None or v is not None:
+            raise ValueError("k and v are given together or not at all")
+        _expect("position", position, torch.int32, (n,))
+        w.position = position.data_ptr()
+        if rope is not None:
+            w.turns, w.rotary_dim, w.interleaved = rope.turns.data_ptr(), rope.rotary_dim, int(rope.interleaved)
+            w.cos_sin_scale = rope.cos_sin_scale
+        for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if t is not None:
+                _expect(name, t, TORCH_DTYPES[self.dtype], (self.head_dim,))
+        w.norm, w.eps, w.q_weight, w.k_weight = int(norm), eps, _opt(q_weight), _opt(k_weight)
+        call = _lib.bind_kv_write(self._kv(), w, self._stream(q, stream))
+        call.tensors = (self.pool, q, k, v, q_out, position, k_slots, v_slots, rope, q_weight, k_weight)
+        return call
+
+    def write(self, *args, **kw):
+        self.bind_write(*args, **kw)()
+
+    # -- attention (slora_attn_decode, slora_attn_prefill)
+    def _attn(self, q, out, k_table, v_table, seq_len, scale, softcap, window, slopes, prefix_len, lse):
+        n_req, max_blocks = k_table.shape
+        a = _lib.Attn()
+        a.n_q_heads = q.shape[1]
+        a.scale = self.head_dim ** -0.5 if scale is None else scale
+        a.softcap, a.window = softcap, window
+        a.q, a.q_token_stride, a.q_head_stride = self._rows("q", q)
+        a.out, a.out_token_stride, a.out_head_stride = self._rows("out", out, q.shape[0], q.shape[1])
+        _expect("k_table", k_table, torch.int32, (n_req, max_blocks))
+        _expect("v_table", v_table, torch.int32, (n_req, max_blocks))
+        _expect("seq_len", seq_len, torch.int32, (n_req,))
+        if slopes is not None:
+            _expect("slopes", slopes, torch.float32, (q.shape[1],))
+        if prefix_len is not None:
+            _expect("prefix_len", prefix_len, torch.int32, (n_req,))
+        if lse is not None:
+            _expect("lse", lse, torch.float32, (q.shape[0], q.shape[1]))
+        a.k_table, a.v_table, a.seq_len = k_table.data_ptr(), v_table.data_ptr(), seq_len.data_ptr()
+        a.slopes, a.prefix_len, a.lse = _opt(slopes), _opt(prefix_len), _opt(lse)
+        return a, self._kv(n_req, max_blocks), (self.pool, q, out, k_table, v_table, seq_len, slopes, prefix_len, lse)
+
+    def _ws(self, kv, a, n_tokens, ws, device):
+        need = _lib.attn_workspace_size(kv, a, n_tokens)
+        return torch.zeros(need, dtype=torch.uint8, device=device) if ws is None else ws
+
+    def bind_decode(self, q: torch.Tensor, out: torch.Tensor, k_table: torch.Tensor, v_table: torch.Tensor,
+                    seq_len: torch.Tensor, scale: Optional[float] = None, softcap: float = 0.0,
+                    window: int = 0, slopes: Optional[torch.Tensor] = None,
+                    prefix_len: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+        if q.shape[0] != k_table.shape[0]:
+            raise ValueError(f"q: {q.shape[0]} rows for {k_table.shape[0]} requests")
+        a, kv, tensors = self._attn(q, out, k_table, v_table, seq_len, scale, softcap, window, slopes,
+                                    prefix_len, lse)
+        ws = self._ws(kv, a, 0, ws, q.device)
+        call = _lib.bind_attn_decode(kv, a, ws.data_ptr(), ws.numel(), self._stream(q, stream))
+        call.tensors = tensors + (ws,)
+        return call
+
+    def decode(self, *args, stream: Optional[torch.cuda.Stream] = None, **kw):
+        call = self.bind_decode(*args, stream=stream, **kw)
+        call()
+        if stream is not None:  # a workspace made here goes back to its own stream's memory
+            call.tensors[-1].record_stream(stream)
+
+    def bind_prefill(self, q: torch.Tensor, out: torch.Tensor, k_table: torch.Tensor, v_table: torch.Tensor,
+                     seq_len: torch.Tensor, q_offsets: torch.Tensor, scale: Optional[float] = None,
+                     softcap: float = 0.0, window: int = 0, slopes: Optional[torch.Tensor] = None,
+                     prefix_len: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     ws: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
+        _expect("q_offsets", q_offsets, torch.int32, (k_table.shape[0] + 1,))
+        a, kv, tensors = self._attn(q, out, k_table, v_table, seq_len, scale, softcap, window, slopes,
+                                    prefix_len, lse)
+        ws = self._ws(kv, a, q.shape[0], ws, q.device)
+        call = _lib.bind_attn_prefill(kv, a, q_offsets.data_ptr(), q.shape[0], ws.data_ptr(), ws.numel(),
+                                      self._stream(q, stream))
+        call.tensors = tensors + (q_offsets, ws)
+        return call
+
+    def prefill(self, *args, stream: Optional[torch.cuda.Stream] = None, **kw):
+        call = self.bind_prefill(*args, stream=stream, **kw)
+        call()
+        if stream is not None:  # a workspace made here goes back to its own stream's memory
+            call.tensors[-1].record_stream(stream)

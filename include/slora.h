@@ -32,7 +32,8 @@
  * of its r rows of A^T (row k = column k of A, length d_in) ceil(d_in/P) pages,
  * then for each of its r rows of B (length d_out) ceil(d_out/P) pages. The last
  * chunk of a row whose length is not a multiple of P leaves the page tail unused.
- * KV-cache pages come from the same free list and are never read by this library.
+ * KV-cache pages come from the same free list; the KV calls read and write them, the
+ * LoRA calls never do.
  * Page tables are int32 arrays; adapter i's entries start at base[i] in that
  * order (A^T rows, chunks ascending; then B rows, chunks ascending).
  *
@@ -442,6 +443,180 @@ int slora_workspace_status(void* ws, void* stream, int32_t* status);
  * results and a set status instead of waiting). */
 int slora_set_wait_limit(int32_t polls);
 
+/* ------------------------------------------------------------------ KV cache and attention
+ * What a serving step does with the pool's KV pages (the S-LoRA overview, section "1.
+ * Unified Paging": KV-cache tensors and adapter weights share one pool). A page holds
+ * the K (or the V) vectors of tokens_per_page consecutive tokens of one request, one
+ * layer: element [i][h][d] of a page is dimension d of KV head h of its i-th token,
+ * tokens_per_page * n_kv_heads * head_dim <= page_elems, the rest of the page unused. A
+ * "plane" is one layer's K or one layer's V; a request's block b holds its tokens
+ * [b * tokens_per_page, (b + 1) * tokens_per_page) and takes one page of every plane.
+ * With tokens_per_page = 1 and kv_pages_per_token planes this is what slora_sched
+ * allocates.
+ *
+ * Every length, table and tensor below is in DEVICE memory and read by the kernels only,
+ * so the calls need no host copy of them, never block the host, allocate nothing and can
+ * be captured into a HIP graph and replayed while the device arrays change. The calls
+ * validate their host arguments; a device value out of range is handled by the kernels:
+ * no memory outside the arrays described here is ever read or written. Calls return
+ * without launching when they have nothing to compute. */
+
+/* The cache as a batch of requests sees it. */
+typedef struct {
+  void* pool;              /* DEVICE: the pool's pages (16-byte aligned) */
+  int64_t n_pages;
+  int32_t page_elems;      /* P, a multiple of 8 */
+  int32_t dtype;           /* SLORA_F16 | SLORA_BF16: pages, q, k, v, out, norm weights */
+  int32_t n_kv_heads;
+  int32_t head_dim;        /* a multiple of 8, 8..256 */
+  int32_t tokens_per_page; /* >= 1 */
+  int32_t n_requests;      /* 0..SLORA_KV_MAX_REQUESTS */
+  int32_t max_blocks;      /* row length of a block table; max_blocks * tokens_per_page <= 2^30 */
+} slora_kv;
+#define SLORA_KV_MAX_REQUESTS 16384
+#define SLORA_KV_MAX_PLANES 4096
+
+/* Block tables, slot maps and positions of a step, from its requests' lengths.
+ *   seq_len[r]  = past_len[r] + new_len[r]                   (negative lengths count as 0)
+ *   q_offsets   = [0, running sums of new_len]: request r's new tokens are rows
+ *                 q_offsets[r] .. q_offsets[r + 1] of the step's token arrays
+ *   token t of request r, the i-th new one:  token_request[t] = r,
+ *                 position[t] = past_len[r] + i
+ *   tables[p][r][b] = page of plane p that holds block b of request r
+ *   slots[p][t] = page * tokens_per_page + position[t] % tokens_per_page, the place of
+ *                 token t in plane p
+ * pages: page ids in allocation order, requests one after the other, block by block,
+ * each block's n_planes ids together. append = 0: all blocks of every request, the
+ * tables are written whole, -1 past a request's last block. append = 1: only the blocks
+ * this step adds (from ceil(past_len / tokens_per_page) on); the rest of the tables,
+ * which the steps before wrote, is read where needed and left as it is.
+ * Entries past the end of `pages` become -1; a slot whose page is outside [0, n_pages)
+ * or past the table is -1. n_tokens is the token arrays' length: rows past the step's
+ * last token get -1 (a fixed n_tokens suits a captured graph), tokens past it are
+ * dropped, and q_offsets never exceeds it. Of `kv` only n_pages, tokens_per_page,
+ * n_requests and max_blocks are used. */
+typedef struct {
+  int32_t n_planes;        /* 1..SLORA_KV_MAX_PLANES */
+  int32_t append;
+  const int32_t* pages;    /* [n_page_ids] */
+  int64_t n_page_ids;
+  const int32_t* past_len; /* [n_requests] tokens cached before this step */
+  const int32_t* new_len;  /* [n_requests] tokens this step adds */
+  int32_t n_tokens;
+  int32_t* tables;         /* [n_planes][n_requests][max_blocks] */
+  int32_t* seq_len;        /* [n_requests] */
+  int32_t* q_offsets;      /* [n_requests + 1] */
+  int32_t* token_request;  /* [n_tokens] */
+  int32_t* position;       /* [n_tokens] */
+  int64_t* slots;          /* [n_planes][n_tokens] */
+} slora_kv_step;
+int slora_kv_tables(const slora_kv* kv, const slora_kv_step* step, void* stream);
+
+/* Rotary position frequencies, in turns per position: turns[i], i < rotary_dim / 2, is
+ * theta^(-2i / rotary_dim) / 2 pi, changed for contexts longer than the model's by
+ *   SLORA_ROPE_NONE    nothing
+ *   SLORA_ROPE_LINEAR  division by factor
+ *   SLORA_ROPE_BASE    theta * factor^(rotary_dim / (rotary_dim - 2)) in theta's place
+ *   SLORA_ROPE_BANDS   by how often the pair turns over original_len positions: at
+ *                      least high_turns times: kept; at most low_turns times: divided by
+ *                      factor; between: the linear blend of the two.
+ * Host only; the caller uploads turns once. They are doubles, and the kernel reduces
+ * position * turns to a fraction of a turn in 64 bits: in 32 bits the angle of position
+ * 10^6 would be off by 0.06 radians. */
+#define SLORA_ROPE_NONE 0
+#define SLORA_ROPE_LINEAR 1
+#define SLORA_ROPE_BASE 2
+#define SLORA_ROPE_BANDS 3
+typedef struct {
+  int32_t rotary_dim; /* a multiple of 8, 8..256 (SLORA_ROPE_BASE: as the others) */
+  int32_t scaling;    /* SLORA_ROPE_* */
+  double theta;       /* > 0 */
+  double factor;      /* > 0 */
+  double original_len, low_turns, high_turns; /* SLORA_ROPE_BANDS: 0 < low_turns < high_turns */
+} slora_rope;
+int slora_rope_turns(const slora_rope* rope, double* turns /* HOST [rotary_dim / 2] */);
+
+/* New tokens' q, k and v, after their projections: per-head norm of q and k, rotary
+ * positions, K and V into the cache, in one pass. For every token t with position[t]
+ * >= 0, and every head x of its q and k:
+ *   norm != 0:   x = x / sqrt(mean(x^2) + eps) * weight      (weight NULL: no product)
+ *   rotation of dimensions [0, rotary_dim), pair i by a = 2 pi position[t] turns[i]:
+ *                (x1, x2) -> cos_sin_scale * (x1 cos a - x2 sin a, x2 cos a + x1 sin a),
+ *                x1, x2 = dimensions i, i + rotary_dim / 2, or 2i, 2i + 1 if interleaved
+ * computed in 32 bits and rounded once; q goes to q_out, k and v (v as it is) to their
+ * slots of the pool. A token whose position is negative is skipped; a slot outside the
+ * pool is not written. Two tokens of one call must not share a slot. q_out may be q
+ * itself (with the same strides). Strides are in elements, every pointer and stride of
+ * q, k, v, q_out a multiple of 16 bytes (as head_dim makes contiguous and packed rows).
+ * k = v = NULL: q alone. n_requests and max_blocks of `kv` are not used. */
+typedef struct {
+  int32_t n_tokens, n_q_heads;
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  const void* k;
+  int64_t k_token_stride, k_head_stride;
+  const void* v;
+  int64_t v_token_stride, v_head_stride;
+  void* q_out;
+  int64_t out_token_stride, out_head_stride;
+  const int32_t* position; /* [n_tokens] */
+  const int64_t* k_slots;  /* [n_tokens], a plane of slora_kv_tables' slots */
+  const int64_t* v_slots;
+  const double* turns;     /* [rotary_dim / 2] */
+  int32_t rotary_dim;      /* 0 (no rotation) or a multiple of 8, <= head_dim */
+  int32_t interleaved;
+  float cos_sin_scale;     /* 1 unless the scaling asks for another */
+  int32_t norm;
+  float eps;
+  const void* q_weight;    /* [head_dim] or NULL */
+  const void* k_weight;
+} slora_qkv;
+int slora_kv_write(const slora_kv* kv, const slora_qkv* qkv, void* stream);
+
+/* Attention over cached keys. Query head h reads KV head h / (n_q_heads / n_kv_heads).
+ * A query at position p of request r sees key j < seq_len[r] when
+ *   (j <= p and (window == 0 or j > p - window)) or (prefix_len and j < prefix_len[r]);
+ * its score is s = scale * q.k_j, then softcap * tanh(s / softcap) if softcap > 0, then
+ * + slopes[h] * (j - p) if slopes is given; out = sum_j softmax(s)_j v_j and lse =
+ * log(sum_j exp(s_j)). Scores, statistics and sums are in 32 bits; the weights exp(s -
+ * max) are rounded to the storage type for the product with V. Keys no query of a row
+ * sees (a request's other rows', unwritten places, the tail of a page) do not touch that
+ * row, whatever they hold. A row that sees no key, or only scores of minus infinity, is
+ * 0 with lse minus infinity. A page id outside the pool reads as NaN, as in the LoRA calls, and a seq_len
+ * outside [0, max_blocks * tokens_per_page] makes the request's rows NaN.
+ * ws: device workspace of slora_attn_workspace_size bytes, 256-byte aligned, contents
+ * irrelevant; calls that share one must be ordered. Strides and pointers as for
+ * slora_qkv. */
+typedef struct {
+  int32_t n_q_heads;         /* a multiple of n_kv_heads */
+  float scale;
+  float softcap;             /* 0 = none */
+  int32_t window;            /* 0 = none */
+  const float* slopes;       /* [n_q_heads] or NULL */
+  const int32_t* prefix_len; /* [n_requests] or NULL */
+  const int32_t* k_table;    /* [n_requests][max_blocks], a plane of slora_kv_tables */
+  const int32_t* v_table;
+  const int32_t* seq_len;    /* [n_requests] */
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  void* out;
+  int64_t out_token_stride, out_head_stride;
+  float* lse;                /* [rows][n_q_heads] or NULL */
+} slora_attn;
+
+/* n_tokens: the prefill call's; 0 sizes for slora_attn_decode. */
+int slora_attn_workspace_size(const slora_kv* kv, const slora_attn* attn, int32_t n_tokens, int64_t* bytes);
+
+/* One new token per request: row r of q and out is request r's token at position
+ * seq_len[r] - 1 (its K and V are in the cache already). */
+int slora_attn_decode(const slora_kv* kv, const slora_attn* attn, void* ws, int64_t ws_bytes, void* stream);
+
+/* The last tokens of every request: rows q_offsets[r] .. q_offsets[r + 1] of q and out
+ * are request r's positions seq_len[r] - new .. seq_len[r] - 1. n_tokens: rows of q and
+ * out; rows no request owns are left as they are. */
+int slora_attn_prefill(const slora_kv* kv, const slora_attn* attn, const int32_t* q_offsets,
+                       int32_t n_tokens, void* ws, int64_t ws_bytes, void* stream);
+
 /* Kernel timing for benchmarks. While enabled (on != 0), every kernel a compute
  * call launches carries two HIP events that the launch itself records on the call's
  * stream when the kernel starts and when it ends (hipExtLaunchKernel), so a timed
@@ -462,7 +637,11 @@ int slora_set_wait_limit(int32_t polls);
 #define SLORA_K_SGMV_FUSED 7
 #define SLORA_K_MIXED_FUSED 8 /* both families of one slora_apply in one launch */
 #define SLORA_K_MULTI_FUSED 9 /* the launch(es) of one slora_apply_multi, timed as one interval */
-#define SLORA_K_COUNT 10
+#define SLORA_K_KV_TABLES 10
+#define SLORA_K_KV_WRITE 11
+#define SLORA_K_ATTN_DECODE 12  /* the launches of one slora_attn_decode, as one interval */
+#define SLORA_K_ATTN_PREFILL 13 /* the launches of one slora_attn_prefill, as one interval */
+#define SLORA_K_COUNT 14
 int slora_timing_enable(int32_t on);
 
 /* Waits for the recorded events, then writes per kernel id the number of timed
