@@ -112,7 +112,7 @@ struct Tile {
 };
 
 template <int DT, int NC>
-__global__ __launch_bounds__(kWaves * 64) void attn_decode_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kernel(AttnArgs a) {
   using S = Shape<NC>;
   constexpr int VD = S::VD, VH = S::VH;
   extern __shared__ float sm_out[];                       // [wave][row][D]

@@ -81,7 +81,7 @@ __device__ __forceinline__ int k_unit(int bn, int chunk, int row) { return chunk
 __device__ __forceinline__ int v_unit(int dims, int kg, int d) { return kg * dims + (d ^ ((d >> 4) & 3)); }
 
 template <int DT, int NC>
-__global__ __launch_bounds__(kThreads) void attn_prefill_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel(AttnArgs a) {
   using S = Shape<NC>;
   constexpr int BN = S::BN, KT = S::KT, kDims = NC * 32;
   __shared__ uint4 sm_k[2][S::kUnits];
