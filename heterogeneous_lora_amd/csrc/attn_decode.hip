@@ -165,7 +165,7 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
   };
   auto put_addr = [&](int t, int32_t page) {
     const int i = tile_begin(t) + (lane & 31);
-    const uint64_t p = key_addr<DT>(a, page, seen.keys.key(min(i, end - 1)), h_off);
+    const uint64_t p = key_addr(a, page, seen.keys.key(min(i, end - 1)), h_off, fill_addr<DT>(false));
     sm_addr[wave][t & 1][lane] = i < end ? p : fill_addr<DT>(true);
   };
   auto fetch = [&](int t, Tile<NC>& x) {

@@ -44,6 +44,11 @@ __device__ __forceinline__ uint32_t div_tpp(const AttnArgs& a, uint32_t n) {
   return a.tpp == 1 ? n : __umulhi(n, a.tpp_magic) >> a.tpp_shift;
 }
 
+// n / group for n < 2^31.
+__device__ __forceinline__ uint32_t div_group(const AttnArgs& a, uint32_t n) {
+  return a.group == 1 ? n : __umulhi(n, a.group_magic) >> a.group_shift;
+}
+
 // The keys the rows of one workgroup see, as one run of indices [0, count): below `pre`
 // the key of that number, from there on that number + gap (a window leaves a hole behind
 // the prefix).
@@ -74,12 +79,13 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, int32_t prefix, int32_t 
   return (j <= p && (a.window == 0 || p - j < a.window)) || j < prefix;
 }
 
-// Address of the first element of key j's vector (head h), given its page id.
-template <int DT>
-__device__ __forceinline__ uint64_t key_addr(const AttnArgs& a, int32_t page, int32_t j, int32_t h_off) {
+// Address of the first element of key j's vector (head h), given its page id; `nans` where
+// the page is outside the pool.
+__device__ __forceinline__ uint64_t key_addr(const AttnArgs& a, int32_t page, int32_t j, int32_t h_off,
+                                             uint64_t nans) {
   const uint32_t in = a.tpp == 1 ? 0u : (uint32_t)j - div_tpp(a, (uint32_t)j) * (uint32_t)a.tpp;
   const uint64_t at = (uint64_t)(a.pool + (int64_t)page * a.P + (uint32_t)(in * (uint32_t)a.row) + h_off);
-  return (uint32_t)page < a.n_pages_u ? at : fill_addr<DT>(false);
+  return (uint32_t)page < a.n_pages_u ? at : nans;
 }
 
 // Score in units of log 2 (weights are exp2 of differences).
@@ -125,6 +131,17 @@ __device__ __forceinline__ float sum16(float x) {
 // Halves of dwords a and b at the same place: (a.lo, b.lo) or (a.hi, b.hi).
 __device__ __forceinline__ uint32_t pair_lo(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+// Two values rounded to nearest even, in one instruction.
+template <int DT>
+__device__ __forceinline__ uint32_t round2(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const f32x2 x = {lo, hi};
+  if constexpr (DT == SLORA_F16)
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, half2_t));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf162_t));
+}
 
 // exp2(m_part - m) as a weight of a partial result: 0 for a part that saw nothing.
 __device__ __forceinline__ float part_weight(float m_part, float m) {

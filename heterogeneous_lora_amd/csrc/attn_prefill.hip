@@ -8,13 +8,17 @@
 // its 4 waves, and walks the keys those rows see in tiles of 64 (32 for heads above 128).
 // Both products are v_mfma_f32_32x32x16 with the keys (or dimensions) as rows and the
 // queries as columns, so a lane keeps one query's statistics, and its scores are, after
-// rounding, the B operand of the second product without an exchange: K's rows lie in LDS
-// with bits 2 and 3 of the key's number swapped, which makes the 8 scores a lane holds
-// for 16 keys those of 8 consecutive keys. V is turned (8 keys x 4 dimensions per thread,
-// in registers) on its way to LDS. Both tiles are laid out in 16-byte units whose index is
-// xored with a few higher bits, so neither side has bank conflicts. Pages are gathered:
-// addresses of a tile's keys are made two tiles ahead, its loads issued one tile ahead
-// into registers and stored to the other LDS buffer after the products.
+// rounding, the B operand of the second product without an exchange: the first product
+// takes K's rows with bits 2 and 3 of the key's number swapped, which makes the 8 scores a
+// lane holds for 16 keys those of 8 consecutive keys.
+//
+// Pages are gathered straight into LDS (global_load_lds, 16 bytes a lane), one tile ahead
+// of the products; the addresses of a tile's keys are made two tiles ahead, its page ids
+// are read three ahead. A tile's rows lie as in the page, in 16-byte units whose places
+// within a row are xored with bits of the row's number: K is read a row to a lane
+// (ds_read_b128), V four keys x 16 dimensions to 16 lanes, turned on the way
+// (ds_read_b64_tr_b16), both without bank conflicts. Two workgroups share a CU, so that one
+// has products to run while the other is at its weights.
 #include "attn_dev.h"
 
 namespace slora {
@@ -32,10 +36,22 @@ template <int NC>
 struct Shape {
   static constexpr int BN = NC <= 4 ? 64 : 32;  // keys of a tile
   static constexpr int KT = BN / 32;
-  static constexpr int kUnits = BN * NC * 4;    // 16-byte units of the K tile, and of the V tile
-  static constexpr int kLoadK = kUnits / kThreads;
-  static constexpr int kBlocksV = BN / 8 * NC * 8;  // 8 keys x 4 dimensions
-  static_assert(kUnits % kThreads == 0 && kBlocksV <= kThreads, "tile loads");
+  static constexpr int CH = NC * 4;             // 16-byte units of a row
+  static constexpr int kUnits = BN * CH;        // of a tile (K or V)
+  static constexpr int kLoads = kUnits / kThreads;
+  static_assert(kUnits % kThreads == 0, "tile loads");
+  // The place of unit c of row `key`: LDS has 16 units a bank row. K is read one unit of
+  // 16 rows at a time, V four units of 4 rows.
+  __device__ static __forceinline__ int k_at(int key, int c) {
+    if constexpr (CH == 12) return c ^ (key >> 2 & 3);
+    else if constexpr (CH % 16) return c ^ (key >> 1 & 7);
+    else return c ^ (key & 15);
+  }
+  __device__ static __forceinline__ int v_at(int key, int c) {
+    if constexpr (CH == 12) return c;
+    else if constexpr (CH % 16) return c ^ (key >> 1 & 1) * 4;
+    else return c ^ (key & 3) * 4;
+  }
 };
 
 struct RowTile {
@@ -70,53 +86,82 @@ __device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int lane, int x)
   return {-1, 0};
 }
 
-// A dword of two storage values holds an infinity or NaN.
+// The halves of a dword of two storage values that hold an infinity or NaN; the rest 0.
 template <int DT>
-__device__ __forceinline__ bool not_finite(uint32_t w) {
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   constexpr uint32_t e = DT == SLORA_F16 ? 0x7C00u : 0x7F80u;
-  return (w & e) == e || (w & (e << 16)) == (e << 16);
+  const uint32_t lo = (w & e) == e ? 0xffffu : 0u, hi = (w & e << 16) == e << 16 ? 0xffff0000u : 0u;
+  return w & (lo | hi);
+}
+// Keeps the compiler from moving what made x into one arm of a later choice, as a branch.
+template <typename T>
+__device__ __forceinline__ T settled(T x) {
+  asm volatile("" : "+v"(x));
+  return x;
 }
 
-__device__ __forceinline__ int k_unit(int bn, int chunk, int row) { return chunk * bn + (row ^ (chunk & 15)); }
-__device__ __forceinline__ int v_unit(int dims, int kg, int d) { return kg * dims + (d ^ ((d >> 4) & 3)); }
+// 16 bytes of every lane from its address to LDS: lane l's land at lds + 16 l. Written out
+// because the compiler, which cannot tell the tile being filled from the one being read,
+// would wait for these loads before every read of LDS; landed() is the wait.
+__device__ __forceinline__ void load_to_lds(uint64_t from, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "{m0}"(lds), "v"(from) : "memory");
+}
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-template <int DT, int NC>
-__global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel(AttnArgs a) {
+typedef __attribute__((address_space(3))) void lds_void;
+__device__ __forceinline__ uint32_t lds_offset(const void* p) { return (uint32_t)(uintptr_t)(lds_void*)p; }
+
+// Four 16-bit values of this lane's column (16 lanes: 4 rows of 16 values, 4 to a lane).
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint2 read_turned(const uint16_t* p) {
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
+}
+
+// What a score passes through between the two products. kPlain: the scale alone, taken in
+// the subtraction of the maximum. kCap: softcap. kAny: a bias that depends on distance, with
+// or without softcap, and scales of zero or below (which would turn a masked -infinity).
+enum Mode { kPlain, kCap, kAny };
+
+template <int DT, int NC, int MODE>
+__global__ __launch_bounds__(kThreads, 2) void attn_prefill_kernel(AttnArgs a) {
   using S = Shape<NC>;
-  constexpr int BN = S::BN, KT = S::KT, kDims = NC * 32;
+  constexpr int BN = S::BN, KT = S::KT, CH = S::CH;
   __shared__ uint4 sm_k[2][S::kUnits];
   __shared__ uint4 sm_v[2][S::kUnits];
   __shared__ uint64_t sm_addr[2][2 * BN];
   __shared__ uint32_t sm_flag[4];  // tile t (mod 4) has infinities or NaN in V that some row must not see
 
-  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m32 = lane & 31, h = lane >> 5;
   const int kv_head = (int)(blockIdx.x % (uint32_t)a.hk);
   const RowTile rt = find_tile(a, lane, (int)(blockIdx.x / (uint32_t)a.hk));
-  if (rt.r < 0) return;
   const int r = __builtin_amdgcn_readfirstlane(rt.r);
+  if (r < 0) return;
   const int row_tile = __builtin_amdgcn_readfirstlane(rt.tile);
   const int q0 = min(max(a.q_offsets[r], 0), a.n_tok), n_new = new_tokens(a, r);
-  const int64_t n_rows = (int64_t)n_new * a.group;
-  const int64_t wg_row = (int64_t)row_tile * kTileM;
-  const int64_t wg_last = min(wg_row + kTileM, n_rows) - 1;
   int32_t n = a.seq[r];
   const bool bad = n < 0 || n > a.max_len;
   if (bad) n = 0;
   const int first_pos = n - n_new;
   const int prefix = a.prefix ? min(max(a.prefix[r], 0), n) : 0;
 
+  // Row i of the tile: token tok0 + (head0 + i) / group, query head (head0 + i) % group.
+  const int rows = (int)min((int64_t)n_new * a.group - (int64_t)row_tile * kTileM, (int64_t)kTileM);
+  const int tile_q = row_tile / a.group, tile_r = row_tile - tile_q * a.group;
+  const int tok0 = tile_q * kTileM + (int)div_group(a, (uint32_t)(tile_r * kTileM));
+  const int head0 = tile_r * kTileM - (tok0 - tile_q * kTileM) * a.group;
+  auto pos_of = [&](int i) { return first_pos + tok0 + (int)div_group(a, (uint32_t)(head0 + min(i, rows - 1))); };
   // this lane's row
-  const int64_t my_row = wg_row + wave * kWaveRows + m32;
-  const int64_t row_c = min(my_row, wg_last);
-  const int tok = (int)(row_c / a.group), head = kv_head * a.group + (int)(row_c - (int64_t)tok * a.group);
-  const int pos = first_pos + tok;
-  const int wave_p0 = first_pos + (int)(min(wg_row + wave * kWaveRows, wg_last) / a.group);
-  const int wave_p1 = first_pos + (int)(min(wg_row + wave * kWaveRows + kWaveRows - 1, wg_last) / a.group);
-  const int wg_p0 = first_pos + (int)(wg_row / a.group), wg_p1 = first_pos + (int)(wg_last / a.group);
+  const int my_row = wave * kWaveRows + m32;
+  const int pos = pos_of(my_row), tok = pos - first_pos;
+  const int head = kv_head * a.group + head0 + min(my_row, rows - 1) - (tok - tok0) * a.group;
+  const int wave_p0 = pos_of(wave * kWaveRows), wave_p1 = pos_of(wave * kWaveRows + kWaveRows - 1);
+  const int wg_p0 = first_pos + tok0, wg_p1 = pos_of(kTileM - 1);
   const Keys keys = n > 0 ? keys_of(a, r, n, wg_p0, wg_p1) : Keys{0, 0, 0};
   const int n_tiles = (keys.count + BN - 1) / BN;
   const int h_off = kv_head * a.D;
+  // In terms of the run's indices the row sees [0, prefix) and [see_lo, see_hi].
+  const int see_hi = pos - keys.gap, see_lo = a.window ? see_hi - a.window + 1 : -1;
 
   // q, as the B operand: lane holds dimensions 16 c + 8 h .. + 7 of its row
   uint4 q[NC * 2];
@@ -128,7 +173,8 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
       q[c] = ld16(d < a.D ? qp + d : kAttnFill.zero);
     }
   }
-  const float slope = a.slopes ? a.slopes[head] * kLog2e : 0.f;
+  const float slope = MODE == kAny && a.slopes ? a.slopes[head] * kLog2e : 0.f;
+  const float mul = MODE == kPlain ? a.scale2 : 1.f;
 
   f32x16 acc[NC];
 #pragma unroll
@@ -137,199 +183,224 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
     for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
   float m = -INFINITY, l = 0.f;
 
-  // addresses of a tile's keys: threads [0, BN) K, [BN, 2 BN) V
-  const int32_t* table = (tid < BN ? a.kt : a.vt) + (int64_t)r * a.max_blocks;
+  // Addresses of a tile's keys: threads [0, BN) K, [BN, 2 BN) V, the others the same again.
+  // (The loop has no branch that lanes could disagree on, one body, and no other place that
+  // changes the accumulators: otherwise the compiler keeps a second set of them, and every
+  // tile pays for copies between the two.)
+  const int my_key = tid % BN;
+  const uint64_t zeros = settled(fill_addr<DT>(true)), nans = settled(fill_addr<DT>(false));
+  const int32_t* table = (tid / BN % 2 ? a.vt : a.kt) + (int64_t)r * a.max_blocks;
   auto page_of = [&](int t) -> int32_t {
-    if (tid >= 2 * BN) return 0;
-    return table[div_tpp(a, (uint32_t)keys.key(min(t * BN + tid % BN, keys.count - 1)))];
+    return table[div_tpp(a, (uint32_t)keys.key(min(t * BN + my_key, keys.count - 1)))];
   };
   auto put_addr = [&](int t, int32_t page) {
-    if (tid >= 2 * BN) return;
-    const int i = t * BN + tid % BN;
-    const uint64_t p = key_addr<DT>(a, page, keys.key(min(i, keys.count - 1)), h_off);
-    sm_addr[t & 1][tid] = i < keys.count ? p : fill_addr<DT>(true);
+    const int i = t * BN + my_key;
+    const uint64_t p = settled(key_addr(a, page, keys.key(min(i, keys.count - 1)), h_off, nans));
+    sm_addr[t & 1][tid % (2 * BN)] = i < keys.count ? p : zeros;
   };
-  uint4 rk[S::kLoadK];
-  uint2 rv[8];
-  const int v_kg = tid / (NC * 8), v_d = tid % (NC * 8) * 4;
-  const bool has_v = tid < S::kBlocksV;
+  const uint32_t lds_k = lds_offset(sm_k) + wave * 1024, lds_v = lds_offset(sm_v) + wave * 1024;
   auto fetch = [&](int t) {
     const uint64_t* ad = sm_addr[t & 1];
+    const uint32_t b = (uint32_t)(t & 1) * S::kUnits * 16;
 #pragma unroll
-    for (int u = 0; u < S::kLoadK; ++u) {
-      const int i = tid + u * kThreads, key = i / (NC * 4), d = i % (NC * 4) * 8;
-      rk[u] = ld16(d < a.D ? (const uint16_t*)ad[key] + d : kAttnFill.zero);
+    for (int u = 0; u < S::kLoads; ++u) {
+      const int i = tid + u * kThreads, key = i / CH, d = S::k_at(key, i % CH) * 8;
+      const uint64_t row = settled(ad[key]);
+      load_to_lds(settled(d < a.D ? row + d * 2 : zeros), lds_k + b + u * kThreads * 16);
     }
-    if (has_v) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint16_t* p = (const uint16_t*)ad[BN + v_kg * 8 + i];
-        rv[i] = *reinterpret_cast<const uint2*>(v_d < a.D ? p + v_d : kAttnFill.zero);
-      }
+    for (int u = 0; u < S::kLoads; ++u) {
+      const int i = tid + u * kThreads, key = i / CH, d = S::v_at(key, i % CH) * 8;
+      const uint64_t row = settled(ad[BN + key]);
+      load_to_lds(settled(d < a.D ? row + d * 2 : zeros), lds_v + b + u * kThreads * 16);
     }
   };
-  // Every row of the workgroup sees every key of tile t.
+  // Every row from position p0 to p1 sees every key of tile t.
   auto all_seen = [&](int t, int p0, int p1) {
     const int i1 = t * BN + BN - 1;
     if (i1 >= keys.count) return false;
     const int j0 = keys.key(t * BN), j1 = keys.key(i1);
     return j1 < prefix || (j1 <= p0 && (a.window == 0 || p1 - j0 < a.window));
   };
-  auto put_tile = [&](int t) {
-    const int b = t & 1;
-#pragma unroll
-    for (int u = 0; u < S::kLoadK; ++u) {
-      const int i = tid + u * kThreads, key = i / (NC * 4), chunk = i % (NC * 4);
-      const int row = (key & ~12) | (key & 4) << 1 | (key & 8) >> 1;
-      sm_k[b][k_unit(BN, chunk, row)] = rk[u];
-    }
-    if (has_v) {
-      bool odd = false;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t x = e < 2 ? rv[2 * i].x : rv[2 * i].y, y = e < 2 ? rv[2 * i + 1].x : rv[2 * i + 1].y;
-          w[i] = e & 1 ? pair_hi(x, y) : pair_lo(x, y);
-          odd |= not_finite<DT>(w[i]);
-        }
-        sm_v[b][v_unit(kDims, v_kg, v_d + e)] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      if (odd && !all_seen(t, wg_p0, wg_p1)) sm_flag[t & 3] = 1;
-    }
-  };
 
-  if (tid < 4) sm_flag[tid] = 0;
+  sm_flag[tid & 3] = 0;
+  int32_t next = 0;
   if (n_tiles > 0) {
     put_addr(0, page_of(0));
+    put_addr(1, page_of(1));
+    next = page_of(2);
     __syncthreads();
     fetch(0);
-    put_addr(1, page_of(1));
-    put_tile(0);
   }
-  __syncthreads();
 
+  const int k_row = (m32 & ~12) | (m32 & 4) << 1 | (m32 & 8) >> 1;
+  const int v_key = h * 8 + (lane >> 2 & 3), v_c = (lane >> 4 & 1) * 2 + (lane >> 1 & 1), v_in = (lane & 1) * 4;
+  // Scores of tile t. Register i of product kt: index t * BN + kt * 32 + 16 (i / 8) + 8 h +
+  // i % 8 of the run.
+  auto scores = [&](int t, f32x16 (&s)[KT]) {
+    const uint4* kb = sm_k[t & 1];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < NC * 2; ++c)
+        s[kt] = mfma32x32<DT>(kb[(kt * 32 + k_row) * CH + S::k_at(k_row, 2 * c + h)], q[c], s[kt]);
+    }
+    if (MODE == kCap || (MODE == kAny && a.cap_out != 0.f)) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[kt][i] = capped(a, s[kt][i]);
+    } else if (MODE == kAny) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[kt][i] *= a.scale2;
+    }
+    if (MODE == kAny) {
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          s[kt][i] += slope * (float)(keys.key(t * BN + kt * 32 + 16 * (i / 8) + 8 * h + i % 8) - pos);
+    }
+  };
+  // The running maximum and sum take the scores in; the weights, as the B operand.
+  auto weights = [&](f32x16 (&s)[KT], uint4 (&p)[KT][2]) {
+    float mx = s[0][0];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kt][i]);
+    mx = max32(mx) * mul;
+    // The maximum is moved only when it has grown by kRescale: until then the weights
+    // reach 2^kRescale, which costs neither range nor precision in 32 bits.
+    if (__any(mx > m + kRescale)) {
+      const float mn = fmaxf(m, mx);
+      const float f = part_weight(m, mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < NC; ++d) acc[d] *= f;
+    }
+    const float ms = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[kt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][i], mul, -ms));
+        l += s[kt][i];
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        p[kt][u] = make_uint4(round2<DT>(s[kt][8 * u], s[kt][8 * u + 1]), round2<DT>(s[kt][8 * u + 2], s[kt][8 * u + 3]),
+                              round2<DT>(s[kt][8 * u + 4], s[kt][8 * u + 5]),
+                              round2<DT>(s[kt][8 * u + 6], s[kt][8 * u + 7]));
+    }
+  };
+  auto add_values = [&](int t, const uint4 (&p)[KT][2]) {
+    const uint16_t* vt = (const uint16_t*)sm_v[t & 1];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int d = 0; d < NC; ++d) {
+          const int key = kt * 32 + u * 16 + v_key;
+          const uint16_t* at = vt + (key * CH + S::v_at(v_key, d * 4 + v_c)) * 8 + v_in;
+          const uint2 x = read_turned(at), y = read_turned(at + 4 * CH * 8);
+          acc[d] = mfma32x32<DT>(make_uint4(x.x, x.y, y.x, y.y), p[kt][u], acc[d]);
+        }
+  };
+
+  bool cleared = false;  // some tile held an infinity or NaN
   for (int t = 0; t < n_tiles; ++t) {
-    const int b = t & 1;
-    int32_t next = 0;
+    landed();         // this wave's share of tile t
+    __syncthreads();  // everyone's; and everyone is done with tile t - 1
     if (t + 1 < n_tiles) {
       fetch(t + 1);
-      next = page_of(t + 2);
+      put_addr(t + 2, next);
+      next = page_of(t + 3);
     }
-    if (tid == 0) sm_flag[(t + 2) & 3] = 0;
-
+    // A tile on some row's border. A weight of zero does not keep an infinity or NaN in V
+    // out of a product, so these are taken out of such a tile and dealt with at the end. No
+    // ordinary tile gets past the look.
+    const bool edge = !all_seen(t, wg_p0, wg_p1);
+    if (edge) {
+      sm_flag[(t + 2) & 3] = 0;
+      uint4* vt = sm_v[t & 1];
+      uint32_t odd = 0;
+#pragma unroll
+      for (int u = 0; u < S::kLoads; ++u) {
+        const uint4 w = vt[tid + u * kThreads];
+        odd |= not_finite<DT>(w.x) | not_finite<DT>(w.y) | not_finite<DT>(w.z) | not_finite<DT>(w.w);
+      }
+      if (__any(odd != 0)) sm_flag[t & 3] = 1;
+      __syncthreads();
+      if (__builtin_amdgcn_readfirstlane(sm_flag[t & 3])) {
+        cleared = true;
+#pragma unroll 1
+        for (int u = 0; u < S::kLoads; ++u) {
+          uint4 w = vt[tid + u * kThreads];
+          w.x ^= not_finite<DT>(w.x);
+          w.y ^= not_finite<DT>(w.y);
+          w.z ^= not_finite<DT>(w.z);
+          w.w ^= not_finite<DT>(w.w);
+          vt[tid + u * kThreads] = w;
+        }
+        __syncthreads();
+      }
+    }
     const int j0 = keys.key(t * BN), j1 = keys.key(min(t * BN + BN, keys.count) - 1);
-    const bool none = j0 >= prefix && (j0 > wave_p1 || (a.window != 0 && wave_p0 - j1 >= a.window));
+    if (j0 >= prefix && (j0 > wave_p1 || (a.window != 0 && wave_p0 - j1 >= a.window))) continue;  // nothing for this wave
+    f32x16 s[KT];
     uint4 p[KT][2];
-    if (!none) {
-      f32x16 s[KT];
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
-#pragma unroll
-        for (int c = 0; c < NC * 2; ++c)
-          s[kt] = mfma32x32<DT>(sm_k[b][k_unit(BN, 2 * c + h, kt * 32 + m32)], q[c], s[kt]);
-      }
-      if (a.cap_out != 0.f) {
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[kt][i] = capped(a, s[kt][i]);
-      } else {
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[kt][i] *= a.scale2;
-      }
-      // register i of product kt: key kt * 32 + 16 (i / 8) + 8 h + i % 8 of the tile
-      if (a.slopes || !all_seen(t, wave_p0, wave_p1)) {
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int at = t * BN + kt * 32 + 16 * (i / 8) + 8 * h + i % 8, j = keys.key(at);
-            const float x = s[kt][i] + slope * (float)(j - pos);
-            s[kt][i] = at < keys.count && sees(a, prefix, pos, j) ? x : -INFINITY;
-          }
-      }
-      float mx = s[0][0];
+    scores(t, s);
+    if (edge) {
+      const int at = t * BN + 8 * h, hi = see_hi - at, lo = see_lo - at, pre = prefix - at;
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kt][i]);
-      mx = max32(mx);
-      // The maximum is moved only when it has grown by kRescale: until then the weights
-      // reach 2^kRescale, which costs neither range nor precision in 32 bits.
-      if (__any(mx > m + kRescale)) {
-        const float mn = fmaxf(m, mx);
-        const float f = part_weight(m, mn);
-        m = mn;
-        l *= f;
-#pragma unroll
-        for (int d = 0; d < NC; ++d) acc[d] *= f;
-      }
-      const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          s[kt][i] = __builtin_amdgcn_exp2f(s[kt][i] - ms);
-          l += s[kt][i];
+          const int k = kt * 32 + 16 * (i / 8) + i % 8;
+          s[kt][i] = (((k <= hi) & (k >= lo)) | (k < pre)) ? s[kt][i] : -INFINITY;
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          p[kt][u] = make_uint4(pack2<DT>(s[kt][8 * u], s[kt][8 * u + 1]), pack2<DT>(s[kt][8 * u + 2], s[kt][8 * u + 3]),
-                                pack2<DT>(s[kt][8 * u + 4], s[kt][8 * u + 5]),
-                                pack2<DT>(s[kt][8 * u + 6], s[kt][8 * u + 7]));
-      }
     }
-    // A weight of zero does not keep an infinity or NaN in V out of a product. Where a key
-    // that some rows must not see holds one, such values are added to the rows that do see
-    // them here (they decide these rows' results, whatever their weight) and cleared from
-    // the tile. No ordinary tile comes here.
-    if (sm_flag[t & 3]) {
-      const uint16_t* vt = (const uint16_t*)sm_v[b];
-      if (!none) {
-        for (int k = 0; k < BN; ++k) {
-          const int at = t * BN + k;
-          const bool on = at < keys.count && sees(a, prefix, pos, keys.key(at));
+    weights(s, p);
+    add_values(t, p);
+  }
+  // The infinities and NaN taken out, to the rows that see them: they decide these rows'
+  // results, whatever their weight.
+  if (cleared) {
+    const int32_t* vt = a.vt + (int64_t)r * a.max_blocks;
+#pragma unroll 1
+    for (int i = 0; i < n_tiles * BN; ++i) {
+      if (i % BN == 0 && all_seen(i / BN, wg_p0, wg_p1)) {
+        i += BN - 1;
+        continue;
+      }
+      if (i >= keys.count) break;
+      const int j = keys.key(i);
+      const uint64_t row = key_addr(a, vt[div_tpp(a, (uint32_t)j)], j, h_off, nans);
+      const uint32_t on = (((i <= see_hi) & (i >= see_lo)) | (i < prefix)) ? ~0u : 0u;
 #pragma unroll
-          for (int d = 0; d < NC; ++d)
+      for (int d = 0; d < NC; ++d)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int dim = d * 32 + 8 * (i / 4) + 4 * h + i % 4;
-              const uint32_t w = vt[v_unit(kDims, k >> 3, dim) * 8 + (k & 7)];
-              if (on && not_finite<DT>(w)) acc[d][i] += lo_f32<DT>(w);
-            }
+        for (int u = 0; u < 4; ++u) {
+          const int dim = d * 32 + 8 * u + 4 * h;
+          const uint64_t w = *(const __attribute__((address_space(1))) uint64_t*)(dim < a.D ? row + dim * 2 : zeros);
+          const uint32_t x0 = not_finite<DT>((uint32_t)w) & on, x1 = not_finite<DT>((uint32_t)(w >> 32)) & on;
+          acc[d][4 * u] += lo_f32<DT>(x0);
+          acc[d][4 * u + 1] += hi_f32<DT>(x0);
+          acc[d][4 * u + 2] += lo_f32<DT>(x1);
+          acc[d][4 * u + 3] += hi_f32<DT>(x1);
         }
-      }
-      __syncthreads();
-      for (int i = tid; i < S::kUnits * 8; i += kThreads) {
-        uint16_t* w = (uint16_t*)sm_v[b] + i;
-        if (not_finite<DT>(*w)) *w = 0;
-      }
-      __syncthreads();
     }
-    if (!none) {
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int d = 0; d < NC; ++d)
-            acc[d] = mfma32x32<DT>(sm_v[b][v_unit(kDims, kt * 4 + u * 2 + h, d * 32 + m32)], p[kt][u], acc[d]);
-    }
-    if (t + 1 < n_tiles) {
-      put_tile(t + 1);
-      put_addr(t + 2, next);
-    }
-    __syncthreads();
   }
 
   l = sum32(l);
-  if (my_row > wg_last) return;
+  if (my_row >= rows) return;
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   uint16_t* o = a.out + (int64_t)(q0 + tok) * a.o_ts + (int64_t)head * a.o_hs;
 #pragma unroll
@@ -341,15 +412,15 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
         float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = bad ? NAN : l == 0.f ? 0.f : acc[d][i + e] * inv;
-        *reinterpret_cast<uint2*>(o + dim) = make_uint2(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]));
+        *reinterpret_cast<uint2*>(o + dim) = make_uint2(round2<DT>(x[0], x[1]), round2<DT>(x[2], x[3]));
       }
     }
   if (a.lse && h == 0)
     a.lse[(int64_t)(q0 + tok) * (a.hk * a.group) + head] = bad ? NAN : m * kLn2 + logf(l);
 }
 
-template <int DT>
-hipError_t launch_dt(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev) {
+template <int DT, int MODE>
+hipError_t launch_mode(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev) {
   const int64_t tiles = ((int64_t)a.n_tok * a.group + kTileM - 1) / kTileM + a.n_req;
   if (tiles * a.hk * kThreads >= kMaxThreads) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(tiles * a.hk));
@@ -358,11 +429,18 @@ hipError_t launch_dt(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev) {
     hipExtLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, ev.start, ev.stop, 0, a);
     return hipGetLastError();
   };
-  return nc <= 2   ? go(attn_prefill_kernel<DT, 2>)
-         : nc == 3 ? go(attn_prefill_kernel<DT, 3>)
-         : nc == 4 ? go(attn_prefill_kernel<DT, 4>)
-         : nc <= 6 ? go(attn_prefill_kernel<DT, 6>)
-                   : go(attn_prefill_kernel<DT, 8>);
+  return nc <= 2   ? go(attn_prefill_kernel<DT, 2, MODE>)
+         : nc == 3 ? go(attn_prefill_kernel<DT, 3, MODE>)
+         : nc == 4 ? go(attn_prefill_kernel<DT, 4, MODE>)
+         : nc <= 6 ? go(attn_prefill_kernel<DT, 6, MODE>)
+                   : go(attn_prefill_kernel<DT, 8, MODE>);
+}
+
+template <int DT>
+hipError_t launch_dt(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev) {
+  return a.slopes || !(a.scale2 > 0.f) ? launch_mode<DT, kAny>(a, s, ev)
+         : a.cap_out != 0.f           ? launch_mode<DT, kCap>(a, s, ev)
+                                      : launch_mode<DT, kPlain>(a, s, ev);
 }
 
 }  // namespace

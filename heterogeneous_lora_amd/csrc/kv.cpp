@@ -168,6 +168,17 @@ int workspace_size(const slora_kv* kv, const slora_attn* at, int32_t n_tokens, i
   return SLORA_OK;
 }
 
+// n / d = umulhi(n, magic) >> shift for n < 2^31, d > 1: with l = ceil(log2 d), magic =
+// floor(2^(31 + l) / d) + 1 and shift l - 1.
+void divisor(int32_t d, uint32_t* magic, uint32_t* shift) {
+  *magic = *shift = 0;
+  if (d < 2) return;
+  int l = 1;
+  while ((int64_t(1) << l) < d) ++l;
+  *magic = (uint32_t)((uint64_t(1) << (31 + l)) / (uint32_t)d + 1);
+  *shift = (uint32_t)(l - 1);
+}
+
 // Checks an attention call and fills the kernels' arguments.
 int attn_args(const char* what, const slora_kv* kv, const slora_attn* at, void* ws, int64_t ws_bytes, int64_t need,
               AttnArgs* a) {
@@ -189,12 +200,7 @@ int attn_args(const char* what, const slora_kv* kv, const slora_attn* at, void* 
   a->n_pages_u = (uint32_t)kv->n_pages;
   a->P = kv->page_elems;
   a->tpp = kv->tokens_per_page;
-  if (a->tpp > 1) {  // ceil(log2 tpp) = l: magic = floor(2^(31 + l) / tpp) + 1, shift l - 1
-    int l = 1;
-    while ((int64_t(1) << l) < a->tpp) ++l;
-    a->tpp_magic = (uint32_t)((uint64_t(1) << (31 + l)) / (uint32_t)a->tpp + 1);
-    a->tpp_shift = (uint32_t)(l - 1);
-  }
+  divisor(a->tpp, &a->tpp_magic, &a->tpp_shift);
   a->hk = kv->n_kv_heads;
   a->D = kv->head_dim;
   a->row = a->hk * a->D;
@@ -202,6 +208,7 @@ int attn_args(const char* what, const slora_kv* kv, const slora_attn* at, void* 
   a->max_blocks = kv->max_blocks;
   a->max_len = kv->max_blocks * kv->tokens_per_page;
   a->group = at->n_q_heads / kv->n_kv_heads;
+  divisor(a->group, &a->group_magic, &a->group_shift);
   a->kt = at->k_table;
   a->vt = at->v_table;
   a->seq = at->seq_len;
