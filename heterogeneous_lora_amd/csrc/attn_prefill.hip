@@ -29,6 +29,7 @@ using namespace dev;
 constexpr int kThreads = 256;
 constexpr int kWaveRows = 32;
 constexpr int kTileM = 128;           // rows of a workgroup
+constexpr int kAhead = 4;              // fragments read ahead of their products
 constexpr float kRescale = 8.0f;      // growth of a maximum (log 2) that moves the sums
 
 // NC: head_dim in pieces of 32, rounded up to an instance.
@@ -40,17 +41,14 @@ struct Shape {
   static constexpr int kUnits = BN * CH;        // of a tile (K or V)
   static constexpr int kLoads = kUnits / kThreads;
   static_assert(kUnits % kThreads == 0, "tile loads");
-  // The place of unit c of row `key`: LDS has 16 units a bank row. K is read one unit of
-  // 16 rows at a time, V four units of 4 rows.
-  __device__ static __forceinline__ int k_at(int key, int c) {
-    if constexpr (CH == 12) return c ^ (key >> 2 & 3);
-    else if constexpr (CH % 16) return c ^ (key >> 1 & 7);
-    else return c ^ (key & 15);
+  // Unit c of row `key` lies at place c ^ k_swap(key) (K) or c ^ v_swap(key) (V) of the row:
+  // LDS has 16 units a bank row, K is read one unit of 16 rows at a time, V four units of 4
+  // rows.
+  __device__ static __forceinline__ int k_swap(int key) {
+    return CH == 12 ? key >> 2 & 3 : CH % 16 ? key >> 1 & 7 : key & 15;
   }
-  __device__ static __forceinline__ int v_at(int key, int c) {
-    if constexpr (CH == 12) return c;
-    else if constexpr (CH % 16) return c ^ (key >> 1 & 1) * 4;
-    else return c ^ (key & 3) * 4;
+  __device__ static __forceinline__ int v_swap(int key) {
+    return CH == 12 ? 0 : CH % 16 ? (key >> 1 & 1) * 4 : (key & 3) * 4;
   }
 };
 
@@ -111,10 +109,15 @@ __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" :::
 typedef __attribute__((address_space(3))) void lds_void;
 __device__ __forceinline__ uint32_t lds_offset(const void* p) { return (uint32_t)(uintptr_t)(lds_void*)p; }
 
+// 16 bytes at an LDS offset.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint4 read_lds(uint32_t at) {
+  return __builtin_bit_cast(uint4, *(const __attribute__((address_space(3))) u32x4*)(uintptr_t)at);
+}
 // Four 16-bit values of this lane's column (16 lanes: 4 rows of 16 values, 4 to a lane).
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ uint2 read_turned(const uint16_t* p) {
-  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)p));
+__device__ __forceinline__ uint2 read_turned(uint32_t at) {
+  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(uintptr_t)at));
 }
 
 // What a score passes through between the two products. kPlain: the scale alone, taken in
@@ -123,7 +126,7 @@ __device__ __forceinline__ uint2 read_turned(const uint16_t* p) {
 enum Mode { kPlain, kCap, kAny };
 
 template <int DT, int NC, int MODE>
-__global__ __launch_bounds__(kThreads, 2) void attn_prefill_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel(AttnArgs a) {
   using S = Shape<NC>;
   constexpr int BN = S::BN, KT = S::KT, CH = S::CH;
   __shared__ uint4 sm_k[2][S::kUnits];
@@ -173,7 +176,7 @@ __global__ __launch_bounds__(kThreads, 2) void attn_prefill_kernel(AttnArgs a) {
       q[c] = ld16(d < a.D ? qp + d : kAttnFill.zero);
     }
   }
-  const float slope = MODE == kAny && a.slopes ? a.slopes[head] * kLog2e : 0.f;
+  float slope = MODE == kAny && a.slopes ? a.slopes[head] * kLog2e : 0.f;
   const float mul = MODE == kPlain ? a.scale2 : 1.f;
 
   f32x16 acc[NC];
@@ -184,35 +187,40 @@ __global__ __launch_bounds__(kThreads, 2) void attn_prefill_kernel(AttnArgs a) {
   float m = -INFINITY, l = 0.f;
 
   // Addresses of a tile's keys: threads [0, BN) K, [BN, 2 BN) V, the others the same again.
+  // The products take K one tile ahead of V, so tile t's turn brings V of tile t + 1 and K of
+  // tile t + 2: place t & 1 holds the addresses for turn t, K's of one tile further on.
   // (The loop has no branch that lanes could disagree on, one body, and no other place that
   // changes the accumulators: otherwise the compiler keeps a second set of them, and every
   // tile pays for copies between the two.)
-  const int my_key = tid % BN;
+  const int my_key = tid % BN, is_v = tid / BN % 2;
   const uint64_t zeros = settled(fill_addr<DT>(true)), nans = settled(fill_addr<DT>(false));
-  const int32_t* table = (tid / BN % 2 ? a.vt : a.kt) + (int64_t)r * a.max_blocks;
-  auto page_of = [&](int t) -> int32_t {
-    return table[div_tpp(a, (uint32_t)keys.key(min(t * BN + my_key, keys.count - 1)))];
-  };
-  auto put_addr = [&](int t, int32_t page) {
-    const int i = t * BN + my_key;
-    const uint64_t p = settled(key_addr(a, page, keys.key(min(i, keys.count - 1)), h_off, nans));
-    sm_addr[t & 1][tid % (2 * BN)] = i < keys.count ? p : zeros;
+  const int32_t* table = (is_v ? a.vt : a.kt) + (int64_t)r * a.max_blocks;
+  auto index_of = [&](int turn) { return (turn + 2 - is_v) * BN + my_key; };  // V at turn -2: below 0
+  auto key_of = [&](int turn) { return keys.key(max(min(index_of(turn), keys.count - 1), 0)); };
+  auto page_of = [&](int turn) -> int32_t { return table[div_tpp(a, (uint32_t)key_of(turn))]; };
+  auto put_addr = [&](int turn, int32_t page) {
+    const int i = index_of(turn);
+    const uint64_t p = settled(key_addr(a, page, key_of(turn), h_off, nans));
+    sm_addr[turn & 1][tid % (2 * BN)] = i < keys.count ? p : zeros;
   };
   const uint32_t lds_k = lds_offset(sm_k) + wave * 1024, lds_v = lds_offset(sm_v) + wave * 1024;
-  auto fetch = [&](int t) {
-    const uint64_t* ad = sm_addr[t & 1];
-    const uint32_t b = (uint32_t)(t & 1) * S::kUnits * 16;
+  // K's units past the head are zeros (their q is 0, but 0 times an infinity is not); V's
+  // make dimensions that are dropped, so any finite or not will do.
+  auto fetch_k = [&](int turn) {
+    const uint32_t b = (uint32_t)(turn & 1) * S::kUnits * 16;
 #pragma unroll
     for (int u = 0; u < S::kLoads; ++u) {
-      const int i = tid + u * kThreads, key = i / CH, d = S::k_at(key, i % CH) * 8;
-      const uint64_t row = settled(ad[key]);
+      const int i = tid + u * kThreads, key = i / CH, d = (i % CH ^ S::k_swap(key)) * 8;
+      const uint64_t row = settled(sm_addr[turn & 1][key]);
       load_to_lds(settled(d < a.D ? row + d * 2 : zeros), lds_k + b + u * kThreads * 16);
     }
+  };
+  auto fetch_v = [&](int turn) {
+    const uint32_t b = (uint32_t)((turn + 1) & 1) * S::kUnits * 16;
 #pragma unroll
     for (int u = 0; u < S::kLoads; ++u) {
-      const int i = tid + u * kThreads, key = i / CH, d = S::v_at(key, i % CH) * 8;
-      const uint64_t row = settled(ad[BN + key]);
-      load_to_lds(settled(d < a.D ? row + d * 2 : zeros), lds_v + b + u * kThreads * 16);
+      const int i = tid + u * kThreads, key = i / CH, d = (i % CH ^ S::v_swap(key)) * 8;
+      load_to_lds(sm_addr[turn & 1][BN + key] + min(d, a.D - 8) * 2, lds_v + b + u * kThreads * 16);
     }
   };
   // Every row from position p0 to p1 sees every key of tile t.
@@ -225,103 +233,117 @@ __global__ __launch_bounds__(kThreads, 2) void attn_prefill_kernel(AttnArgs a) {
 
   sm_flag[tid & 3] = 0;
   int32_t next = 0;
-  if (n_tiles > 0) {
-    put_addr(0, page_of(0));
-    put_addr(1, page_of(1));
-    next = page_of(2);
+  if (n_tiles > 0) {  // turn -2 brings K of tile 0, turn -1 V of tile 0 and K of tile 1
+    put_addr(-2, page_of(-2));
+    put_addr(-1, page_of(-1));
+    next = page_of(0);
     __syncthreads();
-    fetch(0);
+    fetch_k(-2);
+    fetch_v(-1);
+    landed();
+    __syncthreads();
+    fetch_k(-1);
+    put_addr(0, next);
+    next = page_of(1);
   }
 
   const int k_row = (m32 & ~12) | (m32 & 4) << 1 | (m32 & 8) >> 1;
   const int v_key = h * 8 + (lane >> 2 & 3), v_c = (lane >> 4 & 1) * 2 + (lane >> 1 & 1), v_in = (lane & 1) * 4;
-  // Scores of tile t. Register i of product kt: index t * BN + kt * 32 + 16 (i / 8) + 8 h +
-  // i % 8 of the run.
-  auto scores = [&](int t, f32x16 (&s)[KT]) {
-    const uint4* kb = sm_k[t & 1];
+  // Fragments: K's rows (the products of a tile are numbered kt, c), V's dimensions (kt, u,
+  // d). One xor-and-add makes an address from the tile's place; the rest is in the
+  // instruction. (Kept in registers, the addresses would be spilled.)
+  constexpr int kSteps = KT * NC * 2, kPairs = KT * 8, kRow = CH * 16;
+  const uint32_t k_base = lds_offset(sm_k) + k_row * kRow, k_xor = (h ^ S::k_swap(k_row)) * 16;
+  const uint32_t v_base = lds_offset(sm_v) + v_key * kRow + v_c * 16 + v_in * 2, v_xor = S::v_swap(v_key) * 16;
+  auto k_frag = [&](uint32_t place, int i) {
+    const int kt = i / (NC * 2), c = i % (NC * 2);
+    return read_lds((k_xor ^ c * 32) + place + kt * 32 * kRow);
+  };
+  auto v_frag = [&](uint32_t place, int i) {
+    const uint32_t at = (v_xor ^ i % NC * 64) + place + i / NC * 16 * kRow;
+    const uint2 x = read_turned(at), y = read_turned(at + 4 * kRow);
+    return make_uint4(x.x, x.y, y.x, y.y);
+  };
+  // Scores 2 j and 2 j + 1 of a lane, from the products. Register i of product kt: index t *
+  // BN + kt * 32 + 16 (i / 8) + 8 h + i % 8 of the run.
+  auto score_pair = [&](int t, f32x16 (&s)[KT], int j) {
+    const int kt = j / 8;
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
-#pragma unroll
-      for (int c = 0; c < NC * 2; ++c)
-        s[kt] = mfma32x32<DT>(kb[(kt * 32 + k_row) * CH + S::k_at(k_row, 2 * c + h)], q[c], s[kt]);
-    }
-    if (MODE == kCap || (MODE == kAny && a.cap_out != 0.f)) {
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[kt][i] = capped(a, s[kt][i]);
-    } else if (MODE == kAny) {
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[kt][i] *= a.scale2;
-    }
-    if (MODE == kAny) {
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          s[kt][i] += slope * (float)(keys.key(t * BN + kt * 32 + 16 * (i / 8) + 8 * h + i % 8) - pos);
+    for (int e = 0; e < 2; ++e) {
+      const int i = j % 8 * 2 + e;
+      float x = s[kt][i];
+      if (MODE == kCap || (MODE == kAny && a.cap_out != 0.f)) x = capped(a, x);
+      else if (MODE == kAny) x *= a.scale2;
+      if (MODE == kAny) {
+        const int k = kt * 32 + 16 * (i / 8) + i % 8, at = t * BN + 8 * h;
+        x += slope * (float)((k >= keys.pre - at ? keys.gap : 0) + at - pos + k);
+      }
+      s[kt][i] = x;
     }
   };
-  // The running maximum and sum take the scores in; the weights, as the B operand.
-  auto weights = [&](f32x16 (&s)[KT], uint4 (&p)[KT][2]) {
+  // -infinity for what the row must not see of a border tile.
+  auto mask = [&](int t, f32x16 (&s)[KT]) {
+    const int at = t * BN + 8 * h, hi = see_hi - at, lo = see_lo - at, pre = prefix - at;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int k = kt * 32 + 16 * (i / 8) + i % 8;
+        s[kt][i] = (((k <= hi) & (k >= lo)) | (k < pre)) ? s[kt][i] : -INFINITY;
+      }
+  };
+  auto maximum = [&](const f32x16 (&s)[KT]) {
     float mx = s[0][0];
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kt][i]);
-    mx = max32(mx) * mul;
-    // The maximum is moved only when it has grown by kRescale: until then the weights
-    // reach 2^kRescale, which costs neither range nor precision in 32 bits.
-    if (__any(mx > m + kRescale)) {
-      const float mn = fmaxf(m, mx);
-      const float f = part_weight(m, mn);
-      m = mn;
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < NC; ++d) acc[d] *= f;
-    }
-    const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[kt][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][i], mul, -ms));
-        l += s[kt][i];
-      }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        p[kt][u] = make_uint4(round2<DT>(s[kt][8 * u], s[kt][8 * u + 1]), round2<DT>(s[kt][8 * u + 2], s[kt][8 * u + 3]),
-                              round2<DT>(s[kt][8 * u + 4], s[kt][8 * u + 5]),
-                              round2<DT>(s[kt][8 * u + 6], s[kt][8 * u + 7]));
-    }
+    return max32(mx) * mul;
   };
-  auto add_values = [&](int t, const uint4 (&p)[KT][2]) {
-    const uint16_t* vt = (const uint16_t*)sm_v[t & 1];
+  // Weights 2 j and 2 j + 1, their part of the sum and of the B operand.
+  auto weight_pair = [&](const f32x16 (&s)[KT], float ms, uint32_t (&p)[KT * 8], int j) {
+    const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j / 8][j % 8 * 2], mul, -ms));
+    const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j / 8][j % 8 * 2 + 1], mul, -ms));
+    l += x;
+    l += y;
+    p[j] = round2<DT>(x, y);
+  };
+
+  // Tiles this wave's rows see: the first w_tiles.
+  int w_tiles = n_tiles;
+  while (w_tiles > 0) {
+    const int j0 = keys.key((w_tiles - 1) * BN);
+    if (j0 <= wave_p1 || j0 < prefix) break;
+    --w_tiles;
+  }
+  // q is waited for here: a wait inside the loop would be one for the tiles on their way.
+#pragma unroll
+  for (int c = 0; c < NC * 2; ++c) q[c] = __builtin_bit_cast(uint4, settled(__builtin_bit_cast(u32x4, q[c])));
+  slope = settled(slope);
+  f32x16 s[KT];
+  float mx = -INFINITY;
+  if (w_tiles > 0) {
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
 #pragma unroll
-        for (int d = 0; d < NC; ++d) {
-          const int key = kt * 32 + u * 16 + v_key;
-          const uint16_t* at = vt + (key * CH + S::v_at(v_key, d * 4 + v_c)) * 8 + v_in;
-          const uint2 x = read_turned(at), y = read_turned(at + 4 * CH * 8);
-          acc[d] = mfma32x32<DT>(make_uint4(x.x, x.y, y.x, y.y), p[kt][u], acc[d]);
-        }
-  };
-
+    for (int i = 0; i < kSteps; ++i) s[i / (NC * 2)] = mfma32x32<DT>(k_frag(k_base, i), q[i % (NC * 2)], s[i / (NC * 2)]);
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) score_pair(0, s, j);
+    if (!all_seen(0, wg_p0, wg_p1)) mask(0, s);
+    mx = maximum(s);
+  }
   bool cleared = false;  // some tile held an infinity or NaN
   for (int t = 0; t < n_tiles; ++t) {
-    landed();         // this wave's share of tile t
-    __syncthreads();  // everyone's; and everyone is done with tile t - 1
+    landed();         // this wave's share of K of tile t + 1 and V of tile t
+    next = settled(next);  // (waited for here, not behind the loads below)
+    __syncthreads();  // everyone's; and everyone is done with the places about to be filled
     if (t + 1 < n_tiles) {
-      fetch(t + 1);
-      put_addr(t + 2, next);
-      next = page_of(t + 3);
+      fetch_k(t);
+      fetch_v(t);
+      put_addr(t + 1, next);
+      next = page_of(t + 2);
     }
     // A tile on some row's border. A weight of zero does not keep an infinity or NaN in V
     // out of a product, so these are taken out of such a tile and dealt with at the end. No
@@ -352,23 +374,61 @@ __global__ __launch_bounds__(kThreads, 2) void attn_prefill_kernel(AttnArgs a) {
         __syncthreads();
       }
     }
-    const int j0 = keys.key(t * BN), j1 = keys.key(min(t * BN + BN, keys.count) - 1);
-    if (j0 >= prefix && (j0 > wave_p1 || (a.window != 0 && wave_p0 - j1 >= a.window))) continue;  // nothing for this wave
-    f32x16 s[KT];
-    uint4 p[KT][2];
-    scores(t, s);
-    if (edge) {
-      const int at = t * BN + 8 * h, hi = see_hi - at, lo = see_lo - at, pre = prefix - at;
+    if (t >= w_tiles) continue;
+    // The maximum is moved only when it has grown by kRescale: until then the weights
+    // reach 2^kRescale, which costs neither range nor precision in 32 bits.
+    if (__any(mx > m + kRescale)) {
+      const float mn = fmaxf(m, mx);
+      const float f = part_weight(m, mn);
+      m = mn;
+      l *= f;
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int k = kt * 32 + 16 * (i / 8) + i % 8;
-          s[kt][i] = (((k <= hi) & (k >= lo)) | (k < pre)) ? s[kt][i] : -INFINITY;
-        }
+      for (int d = 0; d < NC; ++d) acc[d] *= f;
     }
-    weights(s, p);
-    add_values(t, p);
+    // Two stretches of matrix work, each beside vector work that does not need it: the next
+    // tile's products beside this one's weights, this tile's values beside the next one's
+    // scores. Step by step in this order (the compiler's own puts a fragment's load right
+    // before its product, and waits for each): fragments are read kAhead products early.
+    f32x16 sn[KT];
+    uint32_t p[KT * 8];
+    const float ms = m == -INFINITY ? 0.f : m;
+    const bool edge_next = !all_seen(t + 1, wg_p0, wg_p1);
+    const uint32_t k_place = k_base + ((t + 1) & 1) * S::kUnits * 16, v_place = v_base + (t & 1) * S::kUnits * 16;
+    uint4 frag[kSteps];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sn[kt][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) frag[i] = k_frag(k_place, i);
+    __builtin_amdgcn_sched_barrier(0);
+    uint4 vfrag[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (i + kAhead < kSteps) frag[i + kAhead] = k_frag(k_place, i + kAhead);
+      else vfrag[i + kAhead - kSteps] = v_frag(v_place, i + kAhead - kSteps);
+      sn[i / (NC * 2)] = mfma32x32<DT>(frag[i], q[i % (NC * 2)], sn[i / (NC * 2)]);
+#pragma unroll
+      for (int j = i * kPairs / kSteps; j < (i + 1) * kPairs / kSteps; ++j) weight_pair(s, ms, p, j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (i + kAhead < kSteps) vfrag[i + kAhead] = v_frag(v_place, i + kAhead);
+      const int b = i / NC * 4;
+      acc[i % NC] = mfma32x32<DT>(vfrag[i], make_uint4(p[b], p[b + 1], p[b + 2], p[b + 3]), acc[i % NC]);
+#pragma unroll
+      for (int j = i * kPairs / kSteps; j < (i + 1) * kPairs / kSteps; ++j) score_pair(t + 1, sn, j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // (the compiler would move the sum and the scores behind the branch)
+    l = settled(l);
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) sn[kt] = settled(sn[kt]);
+    if (edge_next) mask(t + 1, sn);
+    mx = maximum(sn);
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt) s[kt] = sn[kt];
   }
   // The infinities and NaN taken out, to the rows that see them: they decide these rows'
   // results, whatever their weight.
