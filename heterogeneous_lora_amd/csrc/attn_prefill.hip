@@ -109,15 +109,17 @@ __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" :::
 typedef __attribute__((address_space(3))) void lds_void;
 __device__ __forceinline__ uint32_t lds_offset(const void* p) { return (uint32_t)(uintptr_t)(lds_void*)p; }
 
-// 16 bytes at an LDS offset.
+// 16 bytes `off` past an LDS offset (a constant `off` is the instruction's).
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ uint4 read_lds(uint32_t at) {
-  return __builtin_bit_cast(uint4, *(const __attribute__((address_space(3))) u32x4*)(uintptr_t)at);
+typedef const __attribute__((address_space(3))) char lds_bytes;
+__device__ __forceinline__ uint4 read_lds(uint32_t at, int off) {
+  return __builtin_bit_cast(uint4, *(const __attribute__((address_space(3))) u32x4*)((lds_bytes*)(uintptr_t)at + off));
 }
 // Four 16-bit values of this lane's column (16 lanes: 4 rows of 16 values, 4 to a lane).
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-__device__ __forceinline__ uint2 read_turned(uint32_t at) {
-  return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(uintptr_t)at));
+__device__ __forceinline__ uint2 read_turned(uint32_t at, int off) {
+  return __builtin_bit_cast(
+      uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)((lds_bytes*)(uintptr_t)at + off)));
 }
 
 // What a score passes through between the two products. kPlain: the scale alone, taken in
@@ -177,7 +179,9 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
     }
   }
   float slope = MODE == kAny && a.slopes ? a.slopes[head] * kLog2e : 0.f;
-  const float mul = MODE == kPlain ? a.scale2 : 1.f;
+  // Scores are s * mul, or s * mul + cap: with softcap s is the reciprocal 1 / (e^(2 x / cap) +
+  // 1) in cap tanh(x / cap) = cap - 2 cap s.
+  const float mul = MODE == kPlain ? a.scale2 : MODE == kCap ? -2.0f * a.cap_out : 1.f;
 
   f32x16 acc[NC];
 #pragma unroll
@@ -234,34 +238,37 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
   sm_flag[tid & 3] = 0;
   int32_t next = 0;
   if (n_tiles > 0) {  // turn -2 brings K of tile 0, turn -1 V of tile 0 and K of tile 1
-    put_addr(-2, page_of(-2));
-    put_addr(-1, page_of(-1));
+    int32_t first = page_of(-2), second = page_of(-1);
     next = page_of(0);
+    put_addr(-2, first);
+    put_addr(-1, second);
     __syncthreads();
     fetch_k(-2);
     fetch_v(-1);
+    if (n_tiles > 1) fetch_k(-1);
     landed();
     __syncthreads();
-    fetch_k(-1);
-    put_addr(0, next);
+    put_addr(0, settled(next));
     next = page_of(1);
   }
 
   const int k_row = (m32 & ~12) | (m32 & 4) << 1 | (m32 & 8) >> 1;
   const int v_key = h * 8 + (lane >> 2 & 3), v_c = (lane >> 4 & 1) * 2 + (lane >> 1 & 1), v_in = (lane & 1) * 4;
-  // Fragments: K's rows (the products of a tile are numbered kt, c), V's dimensions (kt, u,
-  // d). One xor-and-add makes an address from the tile's place; the rest is in the
-  // instruction. (Kept in registers, the addresses would be spilled.)
+  // Fragments: K's rows (the products of a tile are numbered c, kt), V's dimensions (d, kt,
+  // u). One xor and one addition make the address of a c's or d's; the rest is in the
+  // instructions. (Kept in registers, the addresses would be spilled.)
   constexpr int kSteps = KT * NC * 2, kPairs = KT * 8, kRow = CH * 16;
   const uint32_t k_base = lds_offset(sm_k) + k_row * kRow, k_xor = (h ^ S::k_swap(k_row)) * 16;
   const uint32_t v_base = lds_offset(sm_v) + v_key * kRow + v_c * 16 + v_in * 2, v_xor = S::v_swap(v_key) * 16;
+  uint32_t frag_at = 0;
   auto k_frag = [&](uint32_t place, int i) {
-    const int kt = i / (NC * 2), c = i % (NC * 2);
-    return read_lds((k_xor ^ c * 32) + place + kt * 32 * kRow);
+    if (i % KT == 0) frag_at = (k_xor ^ i / KT * 32) + place;
+    return read_lds(frag_at, i % KT * 32 * kRow);
   };
   auto v_frag = [&](uint32_t place, int i) {
-    const uint32_t at = (v_xor ^ i % NC * 64) + place + i / NC * 16 * kRow;
-    const uint2 x = read_turned(at), y = read_turned(at + 4 * kRow);
+    if (i % (KT * 2) == 0) frag_at = (v_xor ^ i / (KT * 2) * 64) + place;
+    const int off = i % (KT * 2) * 16 * kRow;
+    const uint2 x = read_turned(frag_at, off), y = read_turned(frag_at, off + 4 * kRow);
     return make_uint4(x.x, x.y, y.x, y.y);
   };
   // Scores 2 j and 2 j + 1 of a lane, from the products. Register i of product kt: index t *
@@ -272,8 +279,8 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
     for (int e = 0; e < 2; ++e) {
       const int i = j % 8 * 2 + e;
       float x = s[kt][i];
-      if (MODE == kCap || (MODE == kAny && a.cap_out != 0.f)) x = capped(a, x);
-      else if (MODE == kAny) x *= a.scale2;
+      if (MODE == kCap) x = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * a.cap_in) + 1.0f);
+      else if (MODE == kAny) x = a.cap_out != 0.f ? capped(a, x) : x * a.scale2;
       if (MODE == kAny) {
         const int k = kt * 32 + 16 * (i / 8) + i % 8, at = t * BN + 8 * h;
         x += slope * (float)((k >= keys.pre - at ? keys.gap : 0) + at - pos + k);
@@ -289,21 +296,21 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int k = kt * 32 + 16 * (i / 8) + i % 8;
-        s[kt][i] = (((k <= hi) & (k >= lo)) | (k < pre)) ? s[kt][i] : -INFINITY;
+        s[kt][i] = (((k <= hi) & (k >= lo)) | (k < pre)) ? s[kt][i] : MODE == kCap ? INFINITY : -INFINITY;
       }
   };
   auto maximum = [&](const f32x16 (&s)[KT]) {
-    float mx = s[0][0];
+    float x = s[0][0];
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kt][i]);
-    return max32(mx) * mul;
+      for (int i = 0; i < 16; ++i) x = MODE == kCap ? fminf(x, s[kt][i]) : fmaxf(x, s[kt][i]);
+    return MODE == kCap ? __builtin_fmaf(-max32(-x), mul, a.cap_out) : max32(x) * mul;
   };
   // Weights 2 j and 2 j + 1, their part of the sum and of the B operand.
   auto weight_pair = [&](const f32x16 (&s)[KT], float ms, uint32_t (&p)[KT * 8], int j) {
-    const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j / 8][j % 8 * 2], mul, -ms));
-    const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j / 8][j % 8 * 2 + 1], mul, -ms));
+    const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j / 8][j % 8 * 2], mul, ms));
+    const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j / 8][j % 8 * 2 + 1], mul, ms));
     l += x;
     l += y;
     p[j] = round2<DT>(x, y);
@@ -328,7 +335,7 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) s[i / (NC * 2)] = mfma32x32<DT>(k_frag(k_base, i), q[i % (NC * 2)], s[i / (NC * 2)]);
+    for (int i = 0; i < kSteps; ++i) s[i % KT] = mfma32x32<DT>(k_frag(k_base, i), q[i / KT], s[i % KT]);
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) score_pair(0, s, j);
     if (!all_seen(0, wg_p0, wg_p1)) mask(0, s);
@@ -340,7 +347,7 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
     next = settled(next);  // (waited for here, not behind the loads below)
     __syncthreads();  // everyone's; and everyone is done with the places about to be filled
     if (t + 1 < n_tiles) {
-      fetch_k(t);
+      if (t + 2 < n_tiles) fetch_k(t);
       fetch_v(t);
       put_addr(t + 1, next);
       next = page_of(t + 2);
@@ -391,7 +398,7 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
     // before its product, and waits for each): fragments are read kAhead products early.
     f32x16 sn[KT];
     uint32_t p[KT * 8];
-    const float ms = m == -INFINITY ? 0.f : m;
+    const float ms = (MODE == kCap ? a.cap_out : 0.f) - (m == -INFINITY ? 0.f : m);
     const bool edge_next = !all_seen(t + 1, wg_p0, wg_p1);
     const uint32_t k_place = k_base + ((t + 1) & 1) * S::kUnits * 16, v_place = v_base + (t & 1) * S::kUnits * 16;
     uint4 frag[kSteps];
@@ -407,7 +414,7 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
     for (int i = 0; i < kSteps; ++i) {
       if (i + kAhead < kSteps) frag[i + kAhead] = k_frag(k_place, i + kAhead);
       else vfrag[i + kAhead - kSteps] = v_frag(v_place, i + kAhead - kSteps);
-      sn[i / (NC * 2)] = mfma32x32<DT>(frag[i], q[i % (NC * 2)], sn[i / (NC * 2)]);
+      sn[i % KT] = mfma32x32<DT>(frag[i], q[i / KT], sn[i % KT]);
 #pragma unroll
       for (int j = i * kPairs / kSteps; j < (i + 1) * kPairs / kSteps; ++j) weight_pair(s, ms, p, j);
       __builtin_amdgcn_sched_barrier(0);
@@ -415,8 +422,8 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       if (i + kAhead < kSteps) vfrag[i + kAhead] = v_frag(v_place, i + kAhead);
-      const int b = i / NC * 4;
-      acc[i % NC] = mfma32x32<DT>(vfrag[i], make_uint4(p[b], p[b + 1], p[b + 2], p[b + 3]), acc[i % NC]);
+      const int b = i % (KT * 2) * 4, d = i / (KT * 2);
+      acc[d] = mfma32x32<DT>(vfrag[i], make_uint4(p[b], p[b + 1], p[b + 2], p[b + 3]), acc[d]);
 #pragma unroll
       for (int j = i * kPairs / kSteps; j < (i + 1) * kPairs / kSteps; ++j) score_pair(t + 1, sn, j);
       __builtin_amdgcn_sched_barrier(0);
