@@ -208,24 +208,24 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
     sm_addr[turn & 1][tid % (2 * BN)] = i < keys.count ? p : zeros;
   };
   const uint32_t lds_k = lds_offset(sm_k) + wave * 1024, lds_v = lds_offset(sm_v) + wave * 1024;
-  // K's units past the head are zeros (their q is 0, but 0 times an infinity is not); V's
-  // make dimensions that are dropped, so any finite or not will do.
-  auto fetch_k = [&](int turn) {
-    const uint32_t b = (uint32_t)(turn & 1) * S::kUnits * 16;
-#pragma unroll
-    for (int u = 0; u < S::kLoads; ++u) {
-      const int i = tid + u * kThreads, key = i / CH, d = (i % CH ^ S::k_swap(key)) * 8;
-      const uint64_t row = settled(sm_addr[turn & 1][key]);
-      load_to_lds(settled(d < a.D ? row + d * 2 : zeros), lds_k + b + u * kThreads * 16);
+  // One of a turn's loads: K's first, then V's. K's units past the head are zeros (their q is
+  // 0, but 0 times an infinity is not); V's make dimensions that are dropped, so any will do.
+  auto row_of = [&](int turn, int u) {
+    return sm_addr[turn & 1][(u < S::kLoads ? 0 : BN) + (tid + u % S::kLoads * kThreads) / CH];
+  };
+  auto fetch = [&](int turn, int u, uint64_t row) {
+    const int i = tid + u % S::kLoads * kThreads, key = i / CH;
+    if (u < S::kLoads) {
+      const int d = (i % CH ^ S::k_swap(key)) * 8;
+      load_to_lds(settled(d < a.D ? row + d * 2 : zeros), lds_k + ((turn & 1) * S::kUnits + u * kThreads) * 16);
+    } else {
+      const int d = (i % CH ^ S::v_swap(key)) * 8;
+      load_to_lds(row + min(d, a.D - 8) * 2, lds_v + (((turn + 1) & 1) * S::kUnits + (u - S::kLoads) * kThreads) * 16);
     }
   };
-  auto fetch_v = [&](int turn) {
-    const uint32_t b = (uint32_t)((turn + 1) & 1) * S::kUnits * 16;
+  auto fetch_all = [&](int turn, int from, int to) {
 #pragma unroll
-    for (int u = 0; u < S::kLoads; ++u) {
-      const int i = tid + u * kThreads, key = i / CH, d = (i % CH ^ S::v_swap(key)) * 8;
-      load_to_lds(sm_addr[turn & 1][BN + key] + min(d, a.D - 8) * 2, lds_v + b + u * kThreads * 16);
-    }
+    for (int u = from; u < to; ++u) fetch(turn, u, settled(row_of(turn, u)));
   };
   // Every row from position p0 to p1 sees every key of tile t.
   auto all_seen = [&](int t, int p0, int p1) {
@@ -243,9 +243,8 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
     put_addr(-2, first);
     put_addr(-1, second);
     __syncthreads();
-    fetch_k(-2);
-    fetch_v(-1);
-    if (n_tiles > 1) fetch_k(-1);
+    fetch_all(-2, 0, S::kLoads);
+    fetch_all(-1, 0, 2 * S::kLoads);
     landed();
     __syncthreads();
     put_addr(0, settled(next));
@@ -346,12 +345,6 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
     landed();         // this wave's share of K of tile t + 1 and V of tile t
     next = settled(next);  // (waited for here, not behind the loads below)
     __syncthreads();  // everyone's; and everyone is done with the places about to be filled
-    if (t + 1 < n_tiles) {
-      if (t + 2 < n_tiles) fetch_k(t);
-      fetch_v(t);
-      put_addr(t + 1, next);
-      next = page_of(t + 2);
-    }
     // A tile on some row's border. A weight of zero does not keep an infinity or NaN in V
     // out of a product, so these are taken out of such a tile and dealt with at the end. No
     // ordinary tile gets past the look.
@@ -381,7 +374,12 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
         __syncthreads();
       }
     }
-    if (t >= w_tiles) continue;
+    if (t >= w_tiles) {
+      fetch_all(t, 0, 2 * S::kLoads);
+      put_addr(t + 1, next);
+      next = page_of(t + 2);
+      continue;
+    }
     // The maximum is moved only when it has grown by kRescale: until then the weights
     // reach 2^kRescale, which costs neither range nor precision in 32 bits.
     if (__any(mx > m + kRescale)) {
@@ -408,12 +406,18 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
       for (int i = 0; i < 16; ++i) sn[kt][i] = 0.f;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) frag[i] = k_frag(k_place, i);
+    uint64_t row = row_of(t, 0);
     __builtin_amdgcn_sched_barrier(0);
     uint4 vfrag[kSteps];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       if (i + kAhead < kSteps) frag[i + kAhead] = k_frag(k_place, i + kAhead);
       else vfrag[i + kAhead - kSteps] = v_frag(v_place, i + kAhead - kSteps);
+#pragma unroll
+      for (int u = i * 2 * S::kLoads / kSteps; u < (i + 1) * 2 * S::kLoads / kSteps; ++u) {
+        fetch(t, u, row);
+        if (u + 1 < 2 * S::kLoads) row = row_of(t, u + 1);
+      }
       sn[i % KT] = mfma32x32<DT>(frag[i], q[i / KT], sn[i % KT]);
 #pragma unroll
       for (int j = i * kPairs / kSteps; j < (i + 1) * kPairs / kSteps; ++j) weight_pair(s, ms, p, j);
@@ -422,6 +426,8 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       if (i + kAhead < kSteps) vfrag[i + kAhead] = v_frag(v_place, i + kAhead);
+      if (i == kSteps / 2) put_addr(t + 1, next);
+      if (i == kSteps - 1) next = page_of(t + 2);
       const int b = i % (KT * 2) * 4, d = i / (KT * 2);
       acc[d] = mfma32x32<DT>(vfrag[i], make_uint4(p[b], p[b + 1], p[b + 2], p[b + 3]), acc[d]);
 #pragma unroll
@@ -437,6 +443,7 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt) s[kt] = sn[kt];
   }
+  landed();  // (tiles past the last, fetched as zeros)
   // The infinities and NaN taken out, to the rows that see them: they decide these rows'
   // results, whatever their weight.
   if (cleared) {
