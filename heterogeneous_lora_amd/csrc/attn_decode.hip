@@ -41,7 +41,8 @@ __device__ __forceinline__ Seen seen_by(const AttnArgs& a, int r) {
   s.n = a.seq[r];
   s.bad = s.n < 0 || s.n > a.max_len;
   if (s.bad) s.n = 0;
-  s.keys = s.n > 0 ? keys_of(a, r, s.n, s.n - 1, s.n - 1) : Keys{0, 0, 0};
+  const int32_t prefix = a.prefix ? min(max(a.prefix[r], 0), s.n) : 0;
+  s.keys = s.n > 0 ? keys_of(a, prefix, s.n, s.n - 1, s.n - 1) : Keys{0, 0, 0};
   return s;
 }
 

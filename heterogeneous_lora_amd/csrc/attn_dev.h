@@ -57,9 +57,9 @@ struct Keys {
   __device__ __forceinline__ int32_t key(int32_t i) const { return i < pre ? i : i + gap; }
 };
 
-// For rows at positions p_min .. p_max of request r with n cached keys (p_max < n).
-__device__ __forceinline__ Keys keys_of(const AttnArgs& a, int r, int32_t n, int32_t p_min, int32_t p_max) {
-  const int32_t prefix = a.prefix ? min(max(a.prefix[r], 0), n) : 0;
+// For rows at positions p_min .. p_max of a request with n cached keys (p_max < n) and a
+// prefix of 0 .. n.
+__device__ __forceinline__ Keys keys_of(const AttnArgs& a, int32_t prefix, int32_t n, int32_t p_min, int32_t p_max) {
   const int32_t lo = a.window ? max(p_min - a.window + 1, 0) : 0;
   const int32_t end = max(p_max + 1, prefix);
   Keys k;
@@ -72,11 +72,6 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs& a, int r, int32_t n, int
     k.count = end - k.gap;
   }
   return k;
-}
-
-// Whether the row at position p sees key j (j < n); prefix as above.
-__device__ __forceinline__ bool sees(const AttnArgs& a, int32_t prefix, int32_t p, int32_t j) {
-  return (j <= p && (a.window == 0 || p - j < a.window)) || j < prefix;
 }
 
 // Address of the first element of key j's vector (head h), given its page id; `nans` where

@@ -53,20 +53,20 @@ struct Shape {
 };
 
 struct RowTile {
-  int r;       // request, -1: none
-  int tile;    // row tile of the request
+  int r;                   // request, -1: none
+  int tile;                // row tile of the request
+  int q0, n_new, n, prefix;  // its first new token, new tokens, seq_len, prefix_len
 };
 
-// The x-th row tile over all requests.
-__device__ __forceinline__ int new_tokens(const AttnArgs& a, int r) {
-  const int q0 = min(max(a.q_offsets[r], 0), a.n_tok), q1 = min(max(a.q_offsets[r + 1], 0), a.n_tok);
-  return max(q1 - q0, 0);
-}
+// The x-th row tile over all requests. What the kernel needs of the request comes from the
+// same pass: a second round of loads would cost a short prompt more than its products.
 __device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int lane, int x) {
   int before = 0;
   for (int r0 = 0; r0 < a.n_req; r0 += 64) {
-    const int r = r0 + lane;
-    const int c = r < a.n_req ? (int)(((int64_t)new_tokens(a, r) * a.group + kTileM - 1) / kTileM) : 0;
+    const int r = min(r0 + lane, a.n_req - 1);
+    const int q0 = min(max(a.q_offsets[r], 0), a.n_tok), q1 = min(max(a.q_offsets[r + 1], 0), a.n_tok);
+    const int n = a.seq[r], prefix = a.prefix ? a.prefix[r] : 0, n_new = max(q1 - q0, 0);
+    const int c = r0 + lane < a.n_req ? (int)(((int64_t)n_new * a.group + kTileM - 1) / kTileM) : 0;
     int sum = c;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -77,11 +77,12 @@ __device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int lane, int x)
     if (hit) {
       const int l = __builtin_ctzll(hit);
       // later tiles of a request see more keys: they go first
-      return {r0 + l, before + __shfl(sum, l) - 1 - x};
+      return {r0 + l, before + __builtin_amdgcn_readlane(sum, l) - 1 - x, __builtin_amdgcn_readlane(q0, l),
+              __builtin_amdgcn_readlane(n_new, l), __builtin_amdgcn_readlane(n, l), __builtin_amdgcn_readlane(prefix, l)};
     }
-    before += __shfl(sum, 63);
+    before += __builtin_amdgcn_readlane(sum, 63);
   }
-  return {-1, 0};
+  return {-1, 0, 0, 0, 0, 0};
 }
 
 // The halves of a dword of two storage values that hold an infinity or NaN; the rest 0.
@@ -91,6 +92,8 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   const uint32_t lo = (w & e) == e ? 0xffffu : 0u, hi = (w & e << 16) == e << 16 ? 0xffff0000u : 0u;
   return w & (lo | hi);
 }
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2 magnitudes(uint32_t w) { return __builtin_bit_cast(u16x2, w & 0x7fff7fffu); }
 // Keeps the compiler from moving what made x into one arm of a later choice, as a branch.
 template <typename T>
 __device__ __forceinline__ T settled(T x) {
@@ -140,15 +143,12 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
   const int m32 = lane & 31, h = lane >> 5;
   const int kv_head = (int)(blockIdx.x % (uint32_t)a.hk);
   const RowTile rt = find_tile(a, lane, (int)(blockIdx.x / (uint32_t)a.hk));
-  const int r = __builtin_amdgcn_readfirstlane(rt.r);
+  const int r = rt.r, row_tile = rt.tile, q0 = rt.q0, n_new = rt.n_new;
   if (r < 0) return;
-  const int row_tile = __builtin_amdgcn_readfirstlane(rt.tile);
-  const int q0 = min(max(a.q_offsets[r], 0), a.n_tok), n_new = new_tokens(a, r);
-  int32_t n = a.seq[r];
-  const bool bad = n < 0 || n > a.max_len;
-  if (bad) n = 0;
+  const bool bad = rt.n < 0 || rt.n > a.max_len;
+  const int32_t n = bad ? 0 : rt.n;
   const int first_pos = n - n_new;
-  const int prefix = a.prefix ? min(max(a.prefix[r], 0), n) : 0;
+  const int prefix = min(max(rt.prefix, 0), n);
 
   // Row i of the tile: token tok0 + (head0 + i) / group, query head (head0 + i) % group.
   const int rows = (int)min((int64_t)n_new * a.group - (int64_t)row_tile * kTileM, (int64_t)kTileM);
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
   const int head = kv_head * a.group + head0 + min(my_row, rows - 1) - (tok - tok0) * a.group;
   const int wave_p0 = pos_of(wave * kWaveRows), wave_p1 = pos_of(wave * kWaveRows + kWaveRows - 1);
   const int wg_p0 = first_pos + tok0, wg_p1 = pos_of(kTileM - 1);
-  const Keys keys = n > 0 ? keys_of(a, r, n, wg_p0, wg_p1) : Keys{0, 0, 0};
+  const Keys keys = n > 0 ? keys_of(a, prefix, n, wg_p0, wg_p1) : Keys{0, 0, 0};
   const int n_tiles = (keys.count + BN - 1) / BN;
   const int h_off = kv_head * a.D;
   // In terms of the run's indices the row sees [0, prefix) and [see_lo, see_hi].
@@ -290,12 +290,13 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
   // -infinity for what the row must not see of a border tile.
   auto mask = [&](int t, f32x16 (&s)[KT]) {
     const int at = t * BN + 8 * h, hi = see_hi - at, lo = see_lo - at, pre = prefix - at;
+    const float out = MODE == kCap ? INFINITY : -INFINITY;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int k = kt * 32 + 16 * (i / 8) + i % 8;
-        s[kt][i] = (((k <= hi) & (k >= lo)) | (k < pre)) ? s[kt][i] : MODE == kCap ? INFINITY : -INFINITY;
+        s[kt][i] = (((k <= hi) & (k >= lo)) | (k < pre)) ? s[kt][i] : out;
       }
   };
   auto maximum = [&](const f32x16 (&s)[KT]) {
@@ -342,37 +343,39 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
   }
   bool cleared = false;  // some tile held an infinity or NaN
   for (int t = 0; t < n_tiles; ++t) {
-    landed();         // this wave's share of K of tile t + 1 and V of tile t
+    landed();              // this wave's share of K of tile t + 1 and V of tile t
     next = settled(next);  // (waited for here, not behind the loads below)
-    __syncthreads();  // everyone's; and everyone is done with the places about to be filled
     // A tile on some row's border. A weight of zero does not keep an infinity or NaN in V
-    // out of a product, so these are taken out of such a tile and dealt with at the end. No
-    // ordinary tile gets past the look.
+    // out of a product, so these are taken out of such a tile and dealt with at the end.
+    // Every thread looks at what it loaded; no ordinary tile costs more.
     const bool edge = !all_seen(t, wg_p0, wg_p1);
+    uint4* const vt = sm_v[t & 1];
     if (edge) {
-      sm_flag[(t + 2) & 3] = 0;
-      uint4* vt = sm_v[t & 1];
-      uint32_t odd = 0;
+      u16x2 top = {0, 0};
 #pragma unroll
       for (int u = 0; u < S::kLoads; ++u) {
         const uint4 w = vt[tid + u * kThreads];
-        odd |= not_finite<DT>(w.x) | not_finite<DT>(w.y) | not_finite<DT>(w.z) | not_finite<DT>(w.w);
+        top = __builtin_elementwise_max(top, magnitudes(w.x));
+        top = __builtin_elementwise_max(top, magnitudes(w.y));
+        top = __builtin_elementwise_max(top, magnitudes(w.z));
+        top = __builtin_elementwise_max(top, magnitudes(w.w));
       }
-      if (__any(odd != 0)) sm_flag[t & 3] = 1;
-      __syncthreads();
-      if (__builtin_amdgcn_readfirstlane(sm_flag[t & 3])) {
-        cleared = true;
+      if (__any(not_finite<DT>(__builtin_bit_cast(uint32_t, top)) != 0)) sm_flag[t & 3] = 1;
+    }
+    __syncthreads();  // everyone's share; and everyone is done with the places about to be filled
+    if (edge || cleared) sm_flag[(t + 2) & 3] = 0;
+    if (edge && __builtin_amdgcn_readfirstlane(sm_flag[t & 3])) {
+      cleared = true;
 #pragma unroll 1
-        for (int u = 0; u < S::kLoads; ++u) {
-          uint4 w = vt[tid + u * kThreads];
-          w.x ^= not_finite<DT>(w.x);
-          w.y ^= not_finite<DT>(w.y);
-          w.z ^= not_finite<DT>(w.z);
-          w.w ^= not_finite<DT>(w.w);
-          vt[tid + u * kThreads] = w;
-        }
-        __syncthreads();
+      for (int u = 0; u < S::kLoads; ++u) {
+        uint4 w = vt[tid + u * kThreads];
+        w.x ^= not_finite<DT>(w.x);
+        w.y ^= not_finite<DT>(w.y);
+        w.z ^= not_finite<DT>(w.z);
+        w.w ^= not_finite<DT>(w.w);
+        vt[tid + u * kThreads] = w;
       }
+      __syncthreads();
     }
     if (t >= w_tiles) {
       fetch_all(t, 0, 2 * S::kLoads);
