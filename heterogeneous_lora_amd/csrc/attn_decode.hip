@@ -2,11 +2,16 @@
 //
 //   s_j = q . k_j (scaled, capped, biased),  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m)
 //
-// Bound by the bytes of K and V, each read once. A workgroup owns one KV head of one
-// request's run of keys, with the query heads that share it as up to 16 rows; its 4 waves
-// take tiles of 32 keys in turn and keep their own maximum m, sum and output, joined in
-// LDS at the end. When there are few requests, long ones are cut into runs that are joined
-// by a second kernel.
+// Bound by the bytes of K and V, each read once. A wave owns one KV head of one request's
+// run of keys, with the query heads that share it as up to 16 rows, and takes tiles of 32
+// keys. Where there are enough requests to fill the device with one chunk each, the 4 waves
+// of a workgroup take up to 4 neighbouring heads, whose vectors lie together in the pages
+// (5.88 TB/s against 5.45 for 512 requests of 40 heads). Otherwise they share one head's
+// keys, each with its own maximum m, sum and output, joined in LDS at the end, and long
+// requests are cut into chunks (a wave to a head would leave four times the partial
+// results). Their partial results are joined by the workgroup that
+// finishes last (a counter in the workspace), in the chunks' order, so the result does not
+// depend on which one that is.
 //
 // A tile never goes through LDS. v_mfma_f32_16x16x32 with A = K (16 keys x 32 dimensions)
 // and B = q leaves lane l with scores of keys 4 (l / 16) + i of query row l % 16. The two
@@ -26,7 +31,6 @@ using namespace dev;
 
 constexpr int kWaves = 4;
 constexpr int kTile = 32;              // keys of a wave's tile
-constexpr int kRound = kWaves * kTile; // keys a workgroup takes in one round
 constexpr int kRows = 16;
 constexpr float kRescale = 8.0f;       // growth of a maximum (log 2) that moves the sums
 
@@ -36,64 +40,99 @@ struct Seen {
   bool bad;      // seq_len outside the table
 };
 
-__device__ __forceinline__ Seen seen_by(const AttnArgs& a, int r) {
+__device__ __forceinline__ Seen seen_by(const AttnArgs& a, int32_t seq, int32_t prefix) {
   Seen s;
-  s.n = a.seq[r];
+  s.n = seq;
   s.bad = s.n < 0 || s.n > a.max_len;
   if (s.bad) s.n = 0;
-  const int32_t prefix = a.prefix ? min(max(a.prefix[r], 0), s.n) : 0;
-  s.keys = s.n > 0 ? keys_of(a, prefix, s.n, s.n - 1, s.n - 1) : Keys{0, 0, 0};
+  s.keys = s.n > 0 ? keys_of(a, min(max(prefix, 0), s.n), s.n, s.n - 1, s.n - 1) : Keys{0, 0, 0};
   return s;
 }
 
-// Keys of a chunk: all requests' keys spread over the workgroups aimed for, in whole
-// rounds. The same on every wave of the call.
-__device__ __forceinline__ int64_t chunk_keys(const AttnArgs& a, int lane, int units) {
-  int64_t total = 0;
-  for (int r = lane; r < a.n_req; r += 64) total += seen_by(a, r).keys.count;
-  for (int d = 32; d; d >>= 1) total += __shfl_xor(total, d);
-  const int64_t chunks = (a.target + units - 1) / units;
-  const int64_t c = (total + chunks - 1) / chunks;
-  return max((c + kRound - 1) / kRound * kRound, (int64_t)kRound);
-}
-
-__device__ __forceinline__ int chunks_of(int32_t count, int64_t chunk) {
-  return count <= chunk ? 1 : (int)((count + chunk - 1) / chunk);
-}
-
 struct Place {
-  int r, first, n;  // request, its first chunk's number, its chunks
+  int r;           // request, -1: none
+  int first, n;    // its first chunk's number, its chunks
+  int32_t seq, prefix;
 };
 
-// The request whose chunks hold number x (r = -1: past the last).
-__device__ __forceinline__ Place find_chunk(const AttnArgs& a, int lane, int64_t chunk, int x) {
-  int before = 0;
-  for (int r0 = 0; r0 < a.n_req; r0 += 64) {
-    const int r = r0 + lane;
-    const int c = r < a.n_req ? chunks_of(seen_by(a, r).keys.count, chunk) : 0;
-    int sum = c;
+// The number nearest to count / chunk: one key more does not make a chunk of its own.
+__device__ __forceinline__ int chunks_of(int32_t count, int32_t chunk) {
+  return count <= chunk ? 1 : (int)(((uint32_t)count + (uint32_t)chunk / 2) / (uint32_t)chunk);
+}
+
+// The request whose chunks hold number x. A chunk is all requests' keys spread over the
+// workgroups aimed for, in whole rounds; every wave of the call finds the same. A lane
+// takes kHold requests at a time, all their loads in flight at once, and keeps them where
+// one turn covers the call: each turn is one memory latency that nothing hides.
+constexpr int kHold = 8, kTurn = 64 * kHold;
+__device__ __forceinline__ Place find_chunk(const AttnArgs& a, int lane, int x, int round) {
+  int32_t seq[kHold], prefix[kHold], count[kHold];
+  auto load = [&](int r0) {
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(sum, d);
-      if (lane >= d) sum += up;
+    for (int k = 0; k < kHold; ++k) {
+      const int r = min(r0 + lane * kHold + k, a.n_req - 1);
+      seq[k] = a.seq[r];
+      prefix[k] = a.prefix ? a.prefix[r] : 0;
     }
+#pragma unroll
+    for (int k = 0; k < kHold; ++k)
+      count[k] = r0 + lane * kHold + k < a.n_req ? seen_by(a, seq[k], prefix[k]).keys.count : -1;
+  };
+  float total = 0.f;
+  for (int r0 = 0; r0 < a.n_req; r0 += kTurn) {
+    load(r0);
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) total += (float)max(count[k], 0);
+  }
+  // (In 32 bits the keys may be off by a part in 10^6: the chunks past one a request stay a
+  // whole number not above a.chunks, which is what the workspace is sized for.)
+  const float want = wave_sum(total) / (float)a.chunks;
+  const int32_t rounds = want < 1e9f ? (int32_t)want / round + 1 : (1 << 30) / round;
+  const int32_t chunk = rounds * round;
+
+  int before = 0;
+  for (int r0 = 0; r0 < a.n_req; r0 += kTurn) {
+    if (a.n_req > kTurn) load(r0);
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < kHold; ++k) mine += count[k] < 0 ? 0 : chunks_of(count[k], chunk);
+    const int sum = running_sum(mine);
     const uint64_t hit = __ballot(x < before + sum);
     if (hit) {
       const int l = __builtin_ctzll(hit);
-      const int at = __shfl(sum, l), n = __shfl(c, l);
-      return {r0 + l, before + at - n, n};
+      Place p{-1, before + sum - mine, 0, 0, 0};
+      bool found = false;
+#pragma unroll
+      for (int k = 0; k < kHold; ++k) {  // lane l's requests; the other lanes' result is not read
+        const int c = count[k] < 0 ? 0 : chunks_of(count[k], chunk);
+        if (!found && x < p.first + c) {
+          p.r = r0 + lane * kHold + k;
+          p.n = c;
+          p.seq = seq[k];
+          p.prefix = prefix[k];
+          found = true;
+        }
+        if (!found) p.first += c;
+      }
+      return {__builtin_amdgcn_readlane(p.r, l), __builtin_amdgcn_readlane(p.first, l), __builtin_amdgcn_readlane(p.n, l),
+              __builtin_amdgcn_readlane(p.seq, l), __builtin_amdgcn_readlane(p.prefix, l)};
     }
-    before += __shfl(sum, 63);
+    before += __builtin_amdgcn_readlane(sum, 63);
   }
-  return {-1, 0, 0};
+  return {-1, 0, 0, 0, 0};
 }
 
-// The chunks of request r, all requests before it counted.
-__device__ __forceinline__ Place chunks_before(const AttnArgs& a, int lane, int64_t chunk, int r) {
-  int before = 0;
-  for (int i = lane; i < r; i += 64) before += chunks_of(seen_by(a, i).keys.count, chunk);
-  for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
-  return {r, before, chunks_of(seen_by(a, r).keys.count, chunk)};
+// Partial results travel between workgroups, on other XCDs as well: stored and loaded at
+// the device's coherence point.
+__device__ __forceinline__ void put_pair(float* p, float x, float y) {
+  __hip_atomic_store((uint64_t*)p, (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float get_part(const float* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t get_pair(const float* p) {
+  return __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // NC: head_dim in pieces of 32, rounded up to an instance; VD: dimensions a lane loads of a
@@ -116,26 +155,31 @@ template <int DT, int NC>
 __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kernel(AttnArgs a) {
   using S = Shape<NC>;
   constexpr int VD = S::VD, VH = S::VH;
-  extern __shared__ float sm_out[];                       // [wave][row][D]
+  extern __shared__ float sm_out[];                       // [wave][row][D + 4]
   __shared__ uint64_t sm_addr[kWaves][2][64];
   __shared__ float sm_m[kWaves][kRows], sm_l[kWaves][kRows];
+  __shared__ int32_t sm_last;
 
-  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m16 = lane & 15, g = lane >> 4;
+  // a workgroup: `heads` neighbouring KV heads, `phases` waves on each
+  const int heads = a.wg_heads, phases = kWaves / heads, phase = wave / heads;
+  const int round = phases * kTile;
   const int row_groups = (a.group + kRows - 1) / kRows;
-  const int units = a.hk * row_groups;
-  const int unit = (int)(blockIdx.x % (uint32_t)units), x = (int)(blockIdx.x / (uint32_t)units);
-  const int64_t chunk = chunk_keys(a, lane, units);
-  const Place at = find_chunk(a, lane, chunk, x);
+  const int units = a.hk / heads * row_groups;
+  const int unit = (int)(blockIdx.x % (uint32_t)units), x_chunk = (int)(blockIdx.x / (uint32_t)units);
+  const Place at = find_chunk(a, lane, x_chunk, round);
   if (at.r < 0) return;
-  const int r = __builtin_amdgcn_readfirstlane(at.r);
-  const Seen seen = seen_by(a, r);
-  const int kv_head = unit / row_groups, row0 = (unit % row_groups) * kRows;
+  const int r = at.r;
+  const Seen seen = seen_by(a, at.seq, at.prefix);
+  const int kv_head = unit / row_groups * heads + wave % heads, row0 = (unit % row_groups) * kRows;
   const int rows = min(a.group - row0, kRows);
   const int head0 = kv_head * a.group + row0;
   const int h_off = kv_head * a.D;
-  const int begin = (int)((x - at.first) * chunk);
-  const int end = (int)min((int64_t)seen.keys.count, begin + chunk);
+  // its chunks are of one length, in whole rounds (the last ones may be empty)
+  const int32_t count = seen.keys.count;
+  const int32_t length = ((uint32_t)(count + at.n - 1) / (uint32_t)at.n + round - 1) / (uint32_t)round * round;
+  const int begin = min((x_chunk - at.first) * length, count), end = min(begin + length, count);
 
   // q, as the B operand: lane l holds dimensions 32 c + 8 (l / 16) .. + 7 of row l % 16
   uint4 q[NC];
@@ -156,10 +200,10 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
     for (int e = 0; e < VD; ++e) acc[h][e] = {0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;
 
-  const int n_tiles = end > begin + wave * kTile ? (end - begin - wave * kTile + kRound - 1) / kRound : 0;
+  const int n_tiles = end > begin + phase * kTile ? (int)((uint32_t)(end - begin - phase * kTile + round - 1) / (uint32_t)round) : 0;
   // lane l looks up key l % 32 of the tile: its K page (l < 32) or V page
   const int32_t* table = (lane < 32 ? a.kt : a.vt) + (int64_t)r * a.max_blocks;
-  auto tile_begin = [&](int t) { return begin + wave * kTile + t * kRound; };
+  auto tile_begin = [&](int t) { return begin + phase * kTile + t * round; };
   auto page_of = [&](int t) -> int32_t {
     const int i = min(tile_begin(t) + (lane & 31), end - 1);
     return table[div_tpp(a, (uint32_t)seen.keys.key(i))];
@@ -287,14 +331,40 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
     }
   }
 
-  // join the waves
   l = sum32(sum16(l));
+  const int heads_q = a.hk * a.group;
+  if (phases == 1 && at.n == 1) {  // a head of this wave's alone: straight from the registers
+    if (m16 >= rows) return;
+    const int head = head0 + m16;
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    uint16_t* o = a.out + (int64_t)r * a.o_ts + (int64_t)head * a.o_hs;
+#pragma unroll
+    for (int h = 0; h < VH; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int d = h * 128 + (g * 4 + i) * VD;
+        if (d >= a.D) continue;
+        uint32_t w[VD / 2];
+#pragma unroll
+        for (int e = 0; e < VD; e += 2)
+          w[e / 2] = round2<DT>(seen.bad ? NAN : l == 0.f ? 0.f : acc[h][e][i] * inv,
+                                seen.bad ? NAN : l == 0.f ? 0.f : acc[h][e + 1][i] * inv);
+        if constexpr (VD == 8) st16(o + d, make_uint4(w[0], w[1], w[2], w[3]));
+        else *reinterpret_cast<uint2*>(o + d) = make_uint2(w[0], w[1]);
+      }
+    if (a.lse && g == 0) a.lse[(int64_t)r * heads_q + head] = seen.bad ? NAN : m * kLn2 + logf(l);
+    return;
+  }
+
+  // Join the waves of each head. Rows are 4 floats apart from a multiple of 8, so the 16
+  // rows' stores meet no bank twice.
+  const int stride = a.D + 4;
   if (g == 0) {
     sm_m[wave][m16] = m;
     sm_l[wave][m16] = l;
   }
   if (m16 < rows) {
-    float* o = sm_out + ((int64_t)wave * rows + m16) * a.D;
+    float* o = sm_out + (wave * rows + m16) * stride;
 #pragma unroll
     for (int h = 0; h < VH; ++h)
 #pragma unroll
@@ -302,70 +372,101 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
         const int d = h * 128 + (g * 4 + i) * VD;
         if (d < a.D) {
 #pragma unroll
-          for (int e = 0; e < VD; ++e) o[d + e] = acc[h][e][i];
+          for (int e = 0; e < VD; e += 4)
+            *reinterpret_cast<float4*>(o + d + e) = make_float4(acc[h][e][i], acc[h][e + 1][i], acc[h][e + 2][i], acc[h][e + 3][i]);
         }
       }
   }
   __syncthreads();
-  for (int i = tid; i < rows * a.D; i += kWaves * 64) {
-    const int row = i / a.D, d = i - row * a.D;
-    float mt = sm_m[0][row];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) mt = fmaxf(mt, sm_m[w][row]);
-    float o = 0.f, lt = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
+  // A chunk's result: [chunk][query head][m, l, out].
+  const int64_t part_row = a.D + 2, part_chunk = heads_q * part_row;
+  const int pairs = a.D / 2;
+  for (int i = tid; i < heads * rows * pairs; i += kWaves * 64) {
+    const int hr = i / pairs, d = (i - hr * pairs) * 2, hw = hr / rows, row = hr - hw * rows;
+    float mt = -INFINITY, lt = 0.f, x = 0.f, y = 0.f;
+    for (int w = hw; w < kWaves; w += heads) mt = fmaxf(mt, sm_m[w][row]);
+    for (int w = hw; w < kWaves; w += heads) {
       const float f = part_weight(sm_m[w][row], mt);
-      o += f * sm_out[((int64_t)w * rows + row) * a.D + d];
+      const float2 o = *reinterpret_cast<const float2*>(sm_out + (w * rows + row) * stride + d);
       lt += f * sm_l[w][row];
+      x += f * o.x;
+      y += f * o.y;
     }
-    const int head = head0 + row;
+    const int hq = (unit / row_groups * heads + hw) * a.group + row0 + row;
     if (at.n == 1) {
-      const float v = seen.bad ? NAN : lt == 0.f ? 0.f : o / lt;
-      a.out[(int64_t)r * a.o_ts + (int64_t)head * a.o_hs + d] = (uint16_t)to_bits<DT>(v);
-      if (a.lse && d == 0)
-        a.lse[(int64_t)r * (a.hk * a.group) + head] = seen.bad ? NAN : mt * kLn2 + logf(lt);
+      const float inv = lt == 0.f ? 0.f : 1.0f / lt;
+      *reinterpret_cast<uint32_t*>(a.out + (int64_t)r * a.o_ts + (int64_t)hq * a.o_hs + d) =
+          round2<DT>(seen.bad ? NAN : lt == 0.f ? 0.f : x * inv, seen.bad ? NAN : lt == 0.f ? 0.f : y * inv);
+      if (a.lse && d == 0) a.lse[(int64_t)r * heads_q + hq] = seen.bad ? NAN : mt * kLn2 + logf(lt);
     } else {
-      float* part = a.part + ((int64_t)x * (a.hk * a.group) + head) * (a.D + 2);
-      part[2 + d] = o;
-      if (d == 0) {
-        part[0] = mt;
-        part[1] = lt;
+      float* part = a.part + (int64_t)x_chunk * part_chunk + hq * part_row;
+      put_pair(part + 2 + d, x, y);
+      if (d == 0) put_pair(part, mt, lt);
+    }
+  }
+  if (at.n == 1) return;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // stored, before this workgroup counts
+  __syncthreads();
+  // Requests before this one hold at.first - r chunks more than they are: the cut requests'
+  // counters are apart and there are no more than chunks aimed for.
+  if (tid == 0) {
+    int32_t* counter = a.counters + (at.first - r) * units + unit;
+    const int32_t n = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    sm_last = n == at.n - 1;
+    if (n == at.n - 1) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
+  }
+  __syncthreads();
+  if (!__builtin_amdgcn_readfirstlane(sm_last)) return;
+  // rows of all the workgroup's heads, a wave to each in turn
+  for (int i = wave; i < heads * rows; i += kWaves) {
+    const int hq = (unit / row_groups * heads + i / rows) * a.group + row0 + i % rows;
+    const float* part = a.part + (int64_t)at.first * part_chunk + hq * part_row;
+    float mt = -INFINITY;
+    for (int c = lane; c < at.n; c += 64) mt = fmaxf(mt, get_part(part + c * part_chunk));
+    mt = max32(max16(mt));
+    for (int d = 8; d; d >>= 1) mt = fmaxf(mt, __shfl_xor(mt, d));
+    constexpr int kPairs = NC <= 4 ? 1 : 2;  // pairs of dimensions of a lane
+    float o[kPairs][2] = {}, lt = 0.f;
+    for (int c0 = 0; c0 < at.n; c0 += 64) {
+      const float* mine = part + min(c0 + lane, at.n - 1) * part_chunk;
+      const float f = part_weight(get_part(mine), mt), lf = f * get_part(mine + 1);
+      lt += c0 + lane < at.n ? lf : 0.f;
+      const int many = min(64, at.n - c0);
+      for (int c = 0; c < many; c += 8) {  // 8 chunks' loads in flight
+        uint64_t v[8][kPairs];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e)
+            v[j][e] = get_pair(part + (c0 + min(c + j, many - 1)) * part_chunk + 2 + min(lane * 2 + e * 128, a.D - 2));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (c + j >= many) break;
+          const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), c + j));
+#pragma unroll
+          for (int e = 0; e < kPairs; ++e) {
+            o[e][0] += w * __uint_as_float((uint32_t)v[j][e]);
+            o[e][1] += w * __uint_as_float((uint32_t)(v[j][e] >> 32));
+          }
+        }
       }
     }
+    for (int d = 32; d; d >>= 1) lt += __shfl_xor(lt, d);
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) {
+      const int d = lane * 2 + e * 128;
+      if (d < a.D)
+        *reinterpret_cast<uint32_t*>(a.out + (int64_t)r * a.o_ts + (int64_t)hq * a.o_hs + d) =
+            lt == 0.f ? 0u : round2<DT>(o[e][0] / lt, o[e][1] / lt);
+    }
+    if (a.lse && lane == 0) a.lse[(int64_t)r * heads_q + hq] = mt * kLn2 + logf(lt);
   }
-}
-
-// Joins the chunks of requests that were cut: workgroup (request, query head).
-template <int DT>
-__global__ __launch_bounds__(64) void attn_decode_join(AttnArgs a) {
-  const int lane = (int)threadIdx.x;
-  const int heads = a.hk * a.group;
-  const int r = (int)(blockIdx.x / (uint32_t)heads), head = (int)(blockIdx.x % (uint32_t)heads);
-  const int units = a.hk * ((a.group + kRows - 1) / kRows);
-  const int64_t chunk = chunk_keys(a, lane, units);
-  if (chunks_of(seen_by(a, r).keys.count, chunk) == 1) return;
-  const Place at = chunks_before(a, lane, chunk, r);
-  const float* part = a.part + ((int64_t)at.first * heads + head) * (a.D + 2);
-  const int64_t stride = (int64_t)heads * (a.D + 2);
-  float mt = -INFINITY;
-  for (int c = lane; c < at.n; c += 64) mt = fmaxf(mt, part[c * stride]);
-  for (int d = 32; d; d >>= 1) mt = fmaxf(mt, __shfl_xor(mt, d));
-  float lt = 0.f;
-  for (int c = lane; c < at.n; c += 64) lt += part_weight(part[c * stride], mt) * part[c * stride + 1];
-  for (int d = 32; d; d >>= 1) lt += __shfl_xor(lt, d);
-  for (int d = lane; d < a.D; d += 64) {
-    float o = 0.f;
-    for (int c = 0; c < at.n; ++c) o += part_weight(part[c * stride], mt) * part[c * stride + 2 + d];
-    a.out[(int64_t)r * a.o_ts + (int64_t)head * a.o_hs + d] = (uint16_t)to_bits<DT>(lt == 0.f ? 0.f : o / lt);
-  }
-  if (a.lse && lane == 0) a.lse[(int64_t)r * heads + head] = mt * kLn2 + logf(lt);
 }
 
 template <int DT, int NC>
 hipError_t launch_nc(const AttnArgs& a, unsigned grid, hipStream_t s, const LaunchEvents& ev) {
   const int rows = a.group < kRows ? a.group : kRows;
-  const size_t lds = sizeof(float) * kWaves * rows * a.D;
+  const size_t lds = sizeof(float) * kWaves * rows * (a.D + 4);
   if (lds > 48 * 1024) {  // with the static part past the 64 KiB a launch has by default
     const hipError_t e = hipFuncSetAttribute((const void*)attn_decode_kernel<DT, NC>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
@@ -377,24 +478,19 @@ hipError_t launch_nc(const AttnArgs& a, unsigned grid, hipStream_t s, const Laun
 
 template <int DT>
 hipError_t launch_dt(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev) {
-  const int units = a.hk * ((a.group + kRows - 1) / kRows);
-  const int64_t wgs = decode_max_chunks(a.n_req, units) * units;
-  if (wgs * kWaves * 64 >= kMaxThreads || (int64_t)a.n_req * a.hk * a.group * 64 >= kMaxThreads)
-    return hipErrorInvalidConfiguration;
-  const unsigned grid = (unsigned)wgs;
-  LaunchEvents first = ev, second = ev;
-  first.stop = nullptr;
-  second.start = nullptr;
+  const int units = a.hk / a.wg_heads * ((a.group + kRows - 1) / kRows);
+  // No request has more chunks than rounds of keys.
+  const int64_t round = kTile * (kWaves / a.wg_heads);
+  const int64_t most = (a.max_len + round - 1) / round, all = (int64_t)a.n_req * (most > 1 ? most : 1);
+  const int64_t chunks = all < (int64_t)a.n_req + a.chunks ? all : (int64_t)a.n_req + a.chunks;
+  if (chunks * units * kWaves * 64 >= kMaxThreads) return hipErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)(chunks * units);
   const int nc = (a.D + 31) / 32;
-  hipError_t e = nc <= 2   ? launch_nc<DT, 2>(a, grid, s, first)
-                 : nc == 3 ? launch_nc<DT, 3>(a, grid, s, first)
-                 : nc == 4 ? launch_nc<DT, 4>(a, grid, s, first)
-                 : nc <= 6 ? launch_nc<DT, 6>(a, grid, s, first)
-                           : launch_nc<DT, 8>(a, grid, s, first);
-  if (e != hipSuccess) return e;
-  hipExtLaunchKernelGGL((attn_decode_join<DT>), dim3((unsigned)(a.n_req * a.hk * a.group)), dim3(64), 0, s,
-                        second.start, second.stop, 0, a);
-  return hipGetLastError();
+  return nc <= 2   ? launch_nc<DT, 2>(a, grid, s, ev)
+         : nc == 3 ? launch_nc<DT, 3>(a, grid, s, ev)
+         : nc == 4 ? launch_nc<DT, 4>(a, grid, s, ev)
+         : nc <= 6 ? launch_nc<DT, 6>(a, grid, s, ev)
+                   : launch_nc<DT, 8>(a, grid, s, ev);
 }
 
 }  // namespace

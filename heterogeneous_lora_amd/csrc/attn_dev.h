@@ -123,6 +123,33 @@ __device__ __forceinline__ float sum16(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// Sums over lanes 0 .. l of a wave, in registers (a row is 16 lanes; the last two steps
+// carry a row's sum into the next, then the lower half's into the upper).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int lanes_shifted(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int running_sum(int x) {
+  x += lanes_shifted<0x111, 0xf>(x);
+  x += lanes_shifted<0x112, 0xf>(x);
+  x += lanes_shifted<0x114, 0xf>(x);
+  x += lanes_shifted<0x118, 0xf>(x);
+  x += lanes_shifted<0x142, 0xa>(x);
+  x += lanes_shifted<0x143, 0xc>(x);
+  return x;
+}
+// The sum over all lanes, the same on every lane.
+__device__ __forceinline__ float wave_sum(float x) {
+  auto step = [&](int moved) { x += __int_as_float(moved); };
+  step(lanes_shifted<0x111, 0xf>(__float_as_int(x)));
+  step(lanes_shifted<0x112, 0xf>(__float_as_int(x)));
+  step(lanes_shifted<0x114, 0xf>(__float_as_int(x)));
+  step(lanes_shifted<0x118, 0xf>(__float_as_int(x)));
+  step(lanes_shifted<0x142, 0xa>(__float_as_int(x)));
+  step(lanes_shifted<0x143, 0xc>(__float_as_int(x)));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
+
 // Halves of dwords a and b at the same place: (a.lo, b.lo) or (a.hi, b.hi).
 __device__ __forceinline__ uint32_t pair_lo(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }

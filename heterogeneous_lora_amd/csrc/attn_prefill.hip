@@ -67,12 +67,7 @@ __device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int lane, int x)
     const int q0 = min(max(a.q_offsets[r], 0), a.n_tok), q1 = min(max(a.q_offsets[r + 1], 0), a.n_tok);
     const int n = a.seq[r], prefix = a.prefix ? a.prefix[r] : 0, n_new = max(q1 - q0, 0);
     const int c = r0 + lane < a.n_req ? (int)(((int64_t)n_new * a.group + kTileM - 1) / kTileM) : 0;
-    int sum = c;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(sum, d);
-      if (lane >= d) sum += up;
-    }
+    const int sum = running_sum(c);
     const uint64_t hit = __ballot(x < before + sum);
     if (hit) {
       const int l = __builtin_ctzll(hit);

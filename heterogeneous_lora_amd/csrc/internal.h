@@ -277,18 +277,30 @@ struct AttnArgs {
   // prefill
   const int32_t* q_offsets;
   int32_t n_tok;
-  // decode and prefill, rows split over the keys: partial results
-  float* part;
-  int32_t target;           // decode: workgroups to aim for
+  // rows cut into chunks of their keys
+  float* part;              // partial results
+  int32_t* counters;        // finished chunks, all 0 between calls
+  int32_t chunks;           // decode: chunks to aim for, all requests together
+  int32_t wg_heads;         // decode: KV heads of a workgroup (1, 2 or 4)
 };
 // Floats of one row's partial result: max, sum, and the head's dimensions.
 inline int64_t attn_part_floats(int32_t D) { return D + 2; }
-// Chunks of the cached keys a decode call is cut into, at most (all requests together),
-// given KV heads x 16-row groups of query heads.
-constexpr int32_t kDecodeTarget = 1024;
-inline int64_t decode_max_chunks(int32_t n_req, int32_t units) {
-  return (int64_t)n_req + (kDecodeTarget + units - 1) / units;
+// Decode: KV heads of a workgroup, as many of 4 as divide them where the requests alone
+// make enough workgroups, else 1; workgroups that share one chunk of keys; chunks to aim
+// for (kDecodeTarget workgroups).
+constexpr int32_t kDecodeTarget = 512;
+inline int32_t decode_wg_heads(int32_t n_req, int32_t hk, int32_t group) {
+  const int32_t heads = hk % 4 == 0 ? 4 : hk % 2 == 0 ? 2 : 1;
+  return (int64_t)n_req * (hk / heads) * ((group + 15) / 16) >= 2 * kDecodeTarget ? heads : 1;
 }
+inline int32_t decode_units(int32_t n_req, int32_t hk, int32_t group) {
+  return hk / decode_wg_heads(n_req, hk, group) * ((group + 15) / 16);
+}
+inline int32_t decode_chunks(int32_t units) { return (kDecodeTarget + units - 1) / units; }
+// The workspace begins with the counters: decode's are chunks aimed for x units, at most
+// kDecodeTarget + units, and hk + hq / 16 bounds units (hk <= 1024, hq <= 16384).
+constexpr int64_t kAttnCounters = kDecodeTarget + 2048;
+constexpr int64_t kAttnCounterBytes = kAttnCounters * 4;
 hipError_t launch_attn_decode(const AttnArgs& a, int32_t dtype, hipStream_t s, const LaunchEvents& ev);
 hipError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, hipStream_t s, const LaunchEvents& ev);
 hipError_t launch_kv_tables(const slora_kv& kv, const slora_kv_step& st, hipStream_t s, const LaunchEvents& ev);

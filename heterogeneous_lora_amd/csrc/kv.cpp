@@ -149,12 +149,10 @@ int check_heads(const char* what, const slora_kv* kv, const slora_attn* at) {
   return SLORA_OK;
 }
 
-constexpr int64_t kMinWorkspace = 256;
-
 int64_t decode_workspace(const slora_kv* kv, const slora_attn* at) {
-  const int group = at->n_q_heads / kv->n_kv_heads, units = kv->n_kv_heads * ((group + 15) / 16);
-  return kMinWorkspace +
-         decode_max_chunks(kv->n_requests, units) * at->n_q_heads * attn_part_floats(kv->head_dim) * (int64_t)sizeof(float);
+  const int units = decode_units(kv->n_requests, kv->n_kv_heads, at->n_q_heads / kv->n_kv_heads);
+  return kAttnCounterBytes + ((int64_t)kv->n_requests + decode_chunks(units)) * at->n_q_heads *
+                                 attn_part_floats(kv->head_dim) * (int64_t)sizeof(float);
 }
 
 int workspace_size(const slora_kv* kv, const slora_attn* at, int32_t n_tokens, int64_t* bytes) {
@@ -164,7 +162,7 @@ int workspace_size(const slora_kv* kv, const slora_attn* at, int32_t n_tokens, i
   if (n_tokens < 0) return fail(SLORA_E_INVALID, "%s: n_tokens %d < 0", what, n_tokens);
   const int rc = check_heads(what, kv, at);
   if (rc) return rc;
-  *bytes = n_tokens ? kMinWorkspace : decode_workspace(kv, at);
+  *bytes = n_tokens ? kAttnCounterBytes : decode_workspace(kv, at);
   return SLORA_OK;
 }
 
@@ -228,8 +226,10 @@ int attn_args(const char* what, const slora_kv* kv, const slora_attn* at, void* 
   }
   a->window = at->window;
   a->slopes = at->slopes;
-  a->part = (float*)((uint8_t*)ws + kMinWorkspace);
-  a->target = kDecodeTarget;
+  a->counters = (int32_t*)ws;
+  a->part = (float*)((uint8_t*)ws + kAttnCounterBytes);
+  a->wg_heads = decode_wg_heads(a->n_req, a->hk, a->group);
+  a->chunks = decode_chunks(decode_units(a->n_req, a->hk, a->group));
   return SLORA_OK;
 }
 
@@ -259,7 +259,7 @@ int attn_prefill(const slora_kv* kv, const slora_attn* at, const int32_t* q_offs
   if (kv->n_requests == 0 || n_tokens == 0) return SLORA_OK;
   if (!q_offsets) return fail(SLORA_E_INVALID, "%s: q_offsets is NULL", what);
   AttnArgs a;
-  if ((rc = attn_args(what, kv, at, ws, ws_bytes, kMinWorkspace, &a))) return rc;
+  if ((rc = attn_args(what, kv, at, ws, ws_bytes, kAttnCounterBytes, &a))) return rc;
   a.q_offsets = q_offsets;
   a.n_tok = n_tokens;
   const hipStream_t s = (hipStream_t)stream;

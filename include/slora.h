@@ -584,8 +584,8 @@ int slora_kv_write(const slora_kv* kv, const slora_qkv* qkv, void* stream);
  * row, whatever they hold. A row that sees no key, or only scores of minus infinity, is
  * 0 with lse minus infinity. A page id outside the pool reads as NaN, as in the LoRA calls, and a seq_len
  * outside [0, max_blocks * tokens_per_page] makes the request's rows NaN.
- * ws: device workspace of slora_attn_workspace_size bytes, 256-byte aligned, contents
- * irrelevant; calls that share one must be ordered. Strides and pointers as for
+ * ws: device workspace of slora_attn_workspace_size bytes, 256-byte aligned, zero-filled
+ * once by the caller; calls of any shapes may share one, but must be ordered. Strides and pointers as for
  * slora_qkv. */
 typedef struct {
   int32_t n_q_heads;         /* a multiple of n_kv_heads */
