@@ -254,6 +254,16 @@ hipError_t timed_fetch(const FetchPage* pages, int64_t n, uint16_t* pool, int32_
 // ---------------------------------------------------------------- KV cache and attention
 // Threads of one launch must stay below this.
 constexpr int64_t kMaxThreads = int64_t(1) << 32;
+// n / d = umulhi(n, magic) >> shift for n < 2^31, d > 1: with l = ceil(log2 d), magic =
+// floor(2^(31 + l) / d) + 1 and shift l - 1.
+inline void divisor(int32_t d, uint32_t* magic, uint32_t* shift) {
+  *magic = *shift = 0;
+  if (d < 2) return;
+  int l = 1;
+  while ((int64_t(1) << l) < d) ++l;
+  *magic = (uint32_t)((uint64_t(1) << (31 + l)) / (uint32_t)d + 1);
+  *shift = (uint32_t)(l - 1);
+}
 // One attention call as the kernels see it (checked by kv.cpp). Strides in elements.
 struct AttnArgs {
   const uint16_t* pool;

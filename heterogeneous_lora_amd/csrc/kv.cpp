@@ -166,17 +166,6 @@ int workspace_size(const slora_kv* kv, const slora_attn* at, int32_t n_tokens, i
   return SLORA_OK;
 }
 
-// n / d = umulhi(n, magic) >> shift for n < 2^31, d > 1: with l = ceil(log2 d), magic =
-// floor(2^(31 + l) / d) + 1 and shift l - 1.
-void divisor(int32_t d, uint32_t* magic, uint32_t* shift) {
-  *magic = *shift = 0;
-  if (d < 2) return;
-  int l = 1;
-  while ((int64_t(1) << l) < d) ++l;
-  *magic = (uint32_t)((uint64_t(1) << (31 + l)) / (uint32_t)d + 1);
-  *shift = (uint32_t)(l - 1);
-}
-
 // Checks an attention call and fills the kernels' arguments.
 int attn_args(const char* what, const slora_kv* kv, const slora_attn* at, void* ws, int64_t ws_bytes, int64_t need,
               AttnArgs* a) {

@@ -5,31 +5,21 @@
 //
 // The page list comes block by block, each block's planes together; a table row holds one
 // plane's blocks. So the work is a transposition, bound by the bytes of the list and the
-// tables: a workgroup reads a run of blocks (their ids of up to 64 planes lie together in
-// the list), turns it in LDS and writes each plane's part of the row. Where a request's
-// blocks start in the list and its tokens in the step's arrays is the sum of the lengths
-// before it: every workgroup adds them up by itself (at most 16384 of them, L2 hits),
-// which takes less time than another launch and a hand-over through memory.
+// tables: a workgroup copies runs of 64 blocks (one stretch of the list) to LDS and writes
+// each plane's 256 bytes of the row, 16 bytes a lane. Where a request's blocks start in the
+// list and its tokens in the step's arrays is the sum of the lengths before it: every
+// workgroup adds them up by itself (at most 16384 of them, L2 hits), which takes less time
+// than another launch and a hand-over through memory. Short rows, a step's one new block
+// or token, take as many lanes as they need, so that all planes are written at once.
 #include "device_common.h"
 
 namespace slora {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPlanes = 64;       // planes a workgroup turns at once
-constexpr int kTileInts = 4096;   // page ids of one LDS tile
-constexpr int kTileBlocks = 1024; // blocks of one tile at most
-// Rows are padded to an odd stride against bank conflicts; tile_blocks() keeps every
-// (blocks x odd stride) within this.
-constexpr int kLdsInts = 5120;
-
-// Blocks of a tile for `planes` planes: a multiple of 64 when it is not one wave's worth.
-__device__ __forceinline__ int tile_blocks(int planes) {
-  const int n = kTileInts / planes & ~63;
-  return n > kTileBlocks ? kTileBlocks : n < 64 ? 64 : n;
-}
-static_assert(1024 * (4 | 1) <= kLdsInts && 64 * (64 | 1) <= kLdsInts && 640 * (6 | 1) <= kLdsInts,
-              "LDS tile");
+constexpr int kPlanes = 96;   // planes a workgroup turns at once, at most
+constexpr int kBlocks = 64;   // blocks of a tile
+constexpr int kLdsInts = kBlocks * (kPlanes | 1);  // rows of an odd stride: no bank conflicts
 
 struct Sums {
   int64_t blocks, tokens;
@@ -77,14 +67,17 @@ __device__ Sums sums_before(const slora_kv_step& st, int32_t tpp, int r) {
   return s;
 }
 
+// Lanes that take one row of n elements: a power of two up to 64.
+__device__ __forceinline__ int row_lanes_log2(int n) { return n >= 64 ? 6 : n <= 1 ? 0 : 32 - __builtin_clz(n - 1); }
+
 // blockIdx.y = request (n_requests: the rows past the step's tokens), blockIdx.x = its
-// share of the row's tiles, blockIdx.z = group of kPlanes planes.
-__global__ __launch_bounds__(kThreads) void kv_tables_kernel(slora_kv_step st, int64_t n_pages,
-                                                             int32_t tpp, int32_t n_req,
-                                                             int32_t max_blocks) {
+// share of the row's tiles, blockIdx.z = group of planes.
+__global__ __launch_bounds__(kThreads) void kv_tables_kernel(slora_kv_step st, int64_t n_pages, int32_t tpp, int32_t n_req,
+                                                             int32_t max_blocks, int32_t group, uint32_t magic,
+                                                             uint32_t shift) {
   __shared__ int32_t tile[kLdsInts];
   const int r = (int)blockIdx.y, tid = (int)threadIdx.x;
-  const int p0 = (int)blockIdx.z * kPlanes, np = min(st.n_planes - p0, kPlanes);
+  const int p0 = (int)blockIdx.z * group, np = min(st.n_planes - p0, group);
   const int64_t T = st.n_tokens;
   const int sub = (int)blockIdx.x, n_sub = (int)gridDim.x;
 
@@ -106,9 +99,11 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(slora_kv_step st, i
   const int64_t b_begin = st.append ? q.past / tpp : 0;
   const int64_t b_used = q.seq > q.past || !st.append ? min(q.blocks, (int64_t)max_blocks) : b_begin;
   const int64_t b_end = st.append ? b_used : max_blocks;
-  const int tb = tile_blocks(np), stride = np | 1;
-  const int64_t tile0 = b_begin + (int64_t)sub * tb;
+  const int stride = np | 1;
+  const int64_t tile0 = b_begin + (int64_t)sub * kBlocks;
   if (sub != 0 && tile0 >= b_end) return;
+  // 16-byte stores where the rows allow them (a tile begins at a multiple of 64 blocks)
+  const bool wide = !st.append && max_blocks % 4 == 0 && ((uintptr_t)st.tables & 15) == 0;
 
   // Rows past the request's blocks are -1 and need no sums.
   const bool any_used = sub == 0 || tile0 < b_used;
@@ -120,39 +115,53 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(slora_kv_step st, i
     st.q_offsets[r] = (int32_t)min(t_first, T);
   }
 
-  for (int64_t b0 = tile0; b0 < b_end; b0 += (int64_t)n_sub * tb) {
-    const int64_t b1 = min(b0 + tb, b_end);
-    const int n_used = (int)max(min(b1, b_used) - b0, (int64_t)0);
+  for (int64_t b0 = tile0; b0 < b_end; b0 += (int64_t)n_sub * kBlocks) {
+    const int64_t b1 = min(b0 + kBlocks, b_end);
+    const int n = (int)(b1 - b0), n_used = (int)max(min(b1, b_used) - b0, (int64_t)0);
     if (n_used > 0) {
       __syncthreads();  // the previous tile has been read
-      for (int i = tid; i < n_used * np; i += kThreads) {
-        const int b = i / np, p = i - b * np;
-        const int64_t blk = b0 + b;
+      const int64_t at0 = (before.blocks + b0 - q.first) * st.n_planes + p0;
+      for (int i = tid; i < n_used * group; i += kThreads) {
+        const int b = group == 1 ? i : (int)(__umulhi((uint32_t)i, magic) >> shift), p = i - b * group;
+        if (p >= np) continue;
         int32_t page = -1;
-        if (blk >= q.first) {
-          const int64_t at = (before.blocks + blk - q.first) * st.n_planes + p0 + p;
+        if (b0 + b >= q.first) {
+          const int64_t at = at0 + (int64_t)b * st.n_planes + p;
           if (at < st.n_page_ids) page = st.pages[at];
         } else {  // append: the block the step before left part full
-          page = st.tables[((int64_t)(p0 + p) * n_req + r) * max_blocks + blk];
+          page = st.tables[((int64_t)(p0 + p) * n_req + r) * max_blocks + b0 + b];
         }
         tile[b * stride + p] = page;
       }
       __syncthreads();
     }
     // table rows: from the tile, -1 past the request's blocks
-    const int w0 = (int)max(q.first - b0, (int64_t)0);  // append: the part-full block stays
-    const int w1 = (int)(b1 - b0);
-    const int lanes = tb < kThreads ? 64 : kThreads;
-    for (int p = tid / lanes; p < np; p += kThreads / lanes) {
-      int32_t* row = st.tables + ((int64_t)(p0 + p) * n_req + r) * max_blocks + b0;
-      for (int b = w0 + tid % lanes; b < w1; b += lanes) row[b] = b < n_used ? tile[b * stride + p] : -1;
+    if (wide) {
+      for (int p = tid >> 4; p < np; p += kThreads >> 4) {
+        const int b = (tid & 15) * 4;
+        if (b >= n) continue;
+        int4 x;
+        x.x = b < n_used ? tile[b * stride + p] : -1;
+        x.y = b + 1 < n_used ? tile[(b + 1) * stride + p] : -1;
+        x.z = b + 2 < n_used ? tile[(b + 2) * stride + p] : -1;
+        x.w = b + 3 < n_used ? tile[(b + 3) * stride + p] : -1;
+        *reinterpret_cast<int4*>(st.tables + ((int64_t)(p0 + p) * n_req + r) * max_blocks + b0 + b) = x;
+      }
+    } else {
+      const int w0 = (int)max(q.first - b0, (int64_t)0);  // append: the part-full block stays
+      const int log2 = row_lanes_log2(n - w0), lanes = 1 << log2;
+      for (int p = tid >> log2; p < np; p += kThreads >> log2) {
+        int32_t* row = st.tables + ((int64_t)(p0 + p) * n_req + r) * max_blocks + b0;
+        for (int b = w0 + (tid & (lanes - 1)); b < n; b += lanes) row[b] = b < n_used ? tile[b * stride + p] : -1;
+      }
     }
     // slots, positions and ids of the new tokens on these blocks
     const int64_t s0 = max(b0 * tpp, q.past), s1 = min((b0 + n_used) * (int64_t)tpp, q.seq);
     const int64_t at = t_first + s0 - q.past;
     const int n_tok = (int)max(min(s1 - s0, T - at), (int64_t)0);
-    for (int p = tid / lanes; p < np; p += kThreads / lanes) {
-      for (int i = tid % lanes; i < n_tok; i += lanes) {
+    const int log2 = row_lanes_log2(n_tok), lanes = 1 << log2;
+    for (int p = tid >> log2; p < np; p += kThreads >> log2) {
+      for (int i = tid & (lanes - 1); i < n_tok; i += lanes) {
         const int64_t pos = s0 + i;
         const int64_t blk = (uint32_t)pos / (uint32_t)tpp;  // pos < 2^32
         const int32_t page = tile[(int)(blk - b0) * stride + p];
@@ -185,17 +194,21 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(slora_kv_step st, i
 
 hipError_t launch_kv_tables(const slora_kv& kv, const slora_kv_step& st, hipStream_t s,
                             const LaunchEvents& ev) {
-  const int groups = (st.n_planes + kPlanes - 1) / kPlanes;
-  // Shares of a row: enough workgroups to fill the device, no more than a row has tiles of
-  // 64 blocks (new tokens of one request alone, in append mode).
+  const int groups = (st.n_planes + kPlanes - 1) / kPlanes, group = (st.n_planes + groups - 1) / groups;
+  uint32_t magic, shift;
+  divisor(group, &magic, &shift);
+  // Shares of a row: enough workgroups to fill the device, no more than a row has tiles (an
+  // append: than the step's tokens could fill).
   const int64_t rows = (int64_t)(kv.n_requests + 1) * groups;
   int64_t sub = (2048 + rows - 1) / rows;
-  const int64_t tiles = ((int64_t)kv.max_blocks + 63) / 64;
+  int64_t blocks = kv.max_blocks;
+  if (st.append && blocks > st.n_tokens / kv.tokens_per_page + 2) blocks = st.n_tokens / kv.tokens_per_page + 2;
+  const int64_t tiles = (blocks + kBlocks - 1) / kBlocks;
   if (sub > tiles) sub = tiles;
   if (sub < 1) sub = 1;
   hipExtLaunchKernelGGL(kv_tables_kernel, dim3((unsigned)sub, (unsigned)(kv.n_requests + 1), (unsigned)groups),
                         dim3(kThreads), 0, s, ev.start, ev.stop, 0, st, kv.n_pages, kv.tokens_per_page,
-                        kv.n_requests, kv.max_blocks);
+                        kv.n_requests, kv.max_blocks, group, magic, shift);
   return hipGetLastError();
 }
 
