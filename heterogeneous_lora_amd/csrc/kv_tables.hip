@@ -21,6 +21,8 @@ constexpr int kPlanes = 96;   // planes a workgroup turns at once, at most
 constexpr int kBlocks = 64;   // blocks of a tile
 constexpr int kLdsInts = kBlocks * (kPlanes | 1);  // rows of an odd stride: no bank conflicts
 
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
 struct Sums {
   int64_t blocks, tokens;
 };
@@ -140,12 +142,13 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(slora_kv_step st, i
       for (int p = tid >> 4; p < np; p += kThreads >> 4) {
         const int b = (tid & 15) * 4;
         if (b >= n) continue;
-        int4 x;
-        x.x = b < n_used ? tile[b * stride + p] : -1;
-        x.y = b + 1 < n_used ? tile[(b + 1) * stride + p] : -1;
-        x.z = b + 2 < n_used ? tile[(b + 2) * stride + p] : -1;
-        x.w = b + 3 < n_used ? tile[(b + 3) * stride + p] : -1;
-        *reinterpret_cast<int4*>(st.tables + ((int64_t)(p0 + p) * n_req + r) * max_blocks + b0 + b) = x;
+        i32x4 x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = b + e < n_used ? tile[(b + e) * stride + p] : -1;
+        // Past the caches: planes' rows lie megabytes apart, and lines that wait there for
+        // others of their set to be written back cost nearly half the time (560 requests x
+        // 80 planes, 413 MB of tables: 158 us against 282).
+        __builtin_nontemporal_store(x, reinterpret_cast<i32x4*>(st.tables + ((int64_t)(p0 + p) * n_req + r) * max_blocks + b0 + b));
       }
     } else {
       const int w0 = (int)max(q.first - b0, (int64_t)0);  // append: the part-full block stays
