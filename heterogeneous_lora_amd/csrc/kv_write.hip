@@ -18,8 +18,8 @@ namespace slora {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTok = 8;        // tokens of one workgroup at most
-constexpr int kAngles = 512;      // cos / sin pairs in LDS: tokens of a workgroup x pairs
+constexpr int kMaxTok = 2;        // tokens of one workgroup at most
+constexpr int kAngles = kMaxTok * 128;  // cos / sin pairs in LDS
 
 struct Rows {
   const uint16_t* p;
@@ -259,7 +259,7 @@ hipError_t launch_kv_write(const slora_kv& kv, const slora_qkv& w, hipStream_t s
   const int heads = a.hq + 2 * a.hk;
   const int groups = kThreads / (v == 8 ? (g <= 4 ? 4 : g <= 8 ? 8 : 16) : (g <= 8 ? 8 : g <= 16 ? 16 : 32));
   int tpw = 1;
-  while (tpw < kMaxTok && a.n_tok / (2 * tpw) >= 2048 && 2 * tpw * a.pairs <= kAngles) tpw *= 2;
+  while (tpw < kMaxTok && a.n_tok / (2 * tpw) >= 2048) tpw *= 2;
   int split = 1;
   while (split * 2 * groups <= heads + groups && (int64_t)a.n_tok * split < 1024) split *= 2;
   a.tpw = tpw;
