@@ -122,12 +122,6 @@ __device__ __forceinline__ Place find_chunk(const AttnArgs& a, int lane, int x, 
   return {-1, 0, 0, 0, 0};
 }
 
-// Partial results travel between workgroups, on other XCDs as well: stored and loaded at
-// the device's coherence point.
-__device__ __forceinline__ void put_pair(float* p, float x, float y) {
-  __hip_atomic_store((uint64_t*)p, (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x), __ATOMIC_RELAXED,
-                     __HIP_MEMORY_SCOPE_AGENT);
-}
 __device__ __forceinline__ float get_part(const float* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }

@@ -165,6 +165,13 @@ __device__ __forceinline__ uint32_t round2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf162_t));
 }
 
+// Partial results travel between workgroups, on other XCDs as well: stored and loaded at
+// the device's coherence point.
+__device__ __forceinline__ void put_pair(float* p, float x, float y) {
+  __hip_atomic_store((uint64_t*)p, (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // exp2(m_part - m) as a weight of a partial result: 0 for a part that saw nothing.
 __device__ __forceinline__ float part_weight(float m_part, float m) {
   return m_part == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m_part - m);

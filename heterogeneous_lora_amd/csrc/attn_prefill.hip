@@ -55,29 +55,58 @@ struct Shape {
 struct RowTile {
   int r;                   // request, -1: none
   int tile;                // row tile of the request
-  int q0, n_new, n, prefix;  // its first new token, new tokens, seq_len, prefix_len
+  int chunk, chunks;       // which part of the tile's keys, of how many
+  int extra;               // chunks past one a tile, over all tiles before this one
+  int q0, n_new, n, prefix;  // the request's first new token, new tokens, seq_len, prefix_len
 };
 
-// The x-th row tile over all requests. What the kernel needs of the request comes from the
-// same pass: a second round of loads would cost a short prompt more than its products.
+// The x-th chunk over all row tiles. Where the tiles alone do not fill the device, requests
+// with more keys than others are cut into chunks, so that the call makes some a.chunks more
+// of them per KV head. What the kernel needs of the request comes from the same pass: a
+// second round of loads would cost a short prompt more than its products.
+constexpr int kMinChunk = 512;  // keys: some 20 us of products, what joining 16 chunks costs
 __device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int lane, int x) {
-  int before = 0;
-  for (int r0 = 0; r0 < a.n_req; r0 += 64) {
+  int q0 = 0, n_new = 0, n = 0, prefix = 0, tiles = 0, sees = 0;
+  auto load = [&](int r0) {
     const int r = min(r0 + lane, a.n_req - 1);
-    const int q0 = min(max(a.q_offsets[r], 0), a.n_tok), q1 = min(max(a.q_offsets[r + 1], 0), a.n_tok);
-    const int n = a.seq[r], prefix = a.prefix ? a.prefix[r] : 0, n_new = max(q1 - q0, 0);
-    const int c = r0 + lane < a.n_req ? (int)(((int64_t)n_new * a.group + kTileM - 1) / kTileM) : 0;
-    const int sum = running_sum(c);
+    q0 = min(max(a.q_offsets[r], 0), a.n_tok);
+    n_new = max(min(max(a.q_offsets[r + 1], 0), a.n_tok) - q0, 0);
+    n = a.seq[r];
+    prefix = a.prefix ? a.prefix[r] : 0;
+    tiles = r0 + lane < a.n_req ? (int)(((int64_t)n_new * a.group + kTileM - 1) / kTileM) : 0;
+    // keys of its last tile, about
+    sees = n < 0 || n > a.max_len ? 0 : a.window ? (int)min((int64_t)n, (int64_t)a.window + max(prefix, 0) + kTileM) : n;
+  };
+  load(0);
+  float length = 1e30f;
+  if (a.chunks) {
+    float work = (float)tiles * (float)sees;
+    for (int r0 = 64; r0 < a.n_req; r0 += 64) {
+      load(r0);
+      work += (float)tiles * (float)sees;
+    }
+    length = fmaxf(wave_sum(work) / (float)a.chunks, (float)kMinChunk);
+    if (a.n_req > 64) load(0);
+  }
+  int before = 0, extra = 0;
+  for (int r0 = 0;;) {
+    const int chunks = (int)fmaxf((float)sees / length + 0.5f, 1.f);
+    const int mine = tiles * chunks, sum = running_sum(mine), extra_mine = mine - tiles, extra_sum = running_sum(extra_mine);
     const uint64_t hit = __ballot(x < before + sum);
     if (hit) {
       const int l = __builtin_ctzll(hit);
+      auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
+      const int c = of(chunks), i = x - before - of(sum - mine), t = i / c;
       // later tiles of a request see more keys: they go first
-      return {r0 + l, before + __builtin_amdgcn_readlane(sum, l) - 1 - x, __builtin_amdgcn_readlane(q0, l),
-              __builtin_amdgcn_readlane(n_new, l), __builtin_amdgcn_readlane(n, l), __builtin_amdgcn_readlane(prefix, l)};
+      return {r0 + l, of(tiles) - 1 - t, i - t * c, c, extra + of(extra_sum - extra_mine) + t * (c - 1),
+              of(q0), of(n_new), of(n), of(prefix)};
     }
     before += __builtin_amdgcn_readlane(sum, 63);
+    extra += __builtin_amdgcn_readlane(extra_sum, 63);
+    r0 += 64;
+    if (r0 >= a.n_req) return {-1, 0, 0, 1, 0, 0, 0, 0, 0};
+    load(r0);
   }
-  return {-1, 0, 0, 0, 0, 0};
 }
 
 // The halves of a dword of two storage values that hold an infinity or NaN; the rest 0.
@@ -158,7 +187,9 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
   const int wave_p0 = pos_of(wave * kWaveRows), wave_p1 = pos_of(wave * kWaveRows + kWaveRows - 1);
   const int wg_p0 = first_pos + tok0, wg_p1 = pos_of(kTileM - 1);
   const Keys keys = n > 0 ? keys_of(a, prefix, n, wg_p0, wg_p1) : Keys{0, 0, 0};
-  const int n_tiles = (keys.count + BN - 1) / BN;
+  // this chunk's tiles of keys
+  const int all_tiles = (keys.count + BN - 1) / BN, per_chunk = (all_tiles + rt.chunks - 1) / rt.chunks;
+  const int first_tile = min(rt.chunk * per_chunk, all_tiles), n_tiles = min(first_tile + per_chunk, all_tiles);
   const int h_off = kv_head * a.D;
   // In terms of the run's indices the row sees [0, prefix) and [see_lo, see_hi].
   const int see_hi = pos - keys.gap, see_lo = a.window ? see_hi - a.window + 1 : -1;
@@ -232,18 +263,19 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
 
   sm_flag[tid & 3] = 0;
   int32_t next = 0;
-  if (n_tiles > 0) {  // turn -2 brings K of tile 0, turn -1 V of tile 0 and K of tile 1
-    int32_t first = page_of(-2), second = page_of(-1);
-    next = page_of(0);
-    put_addr(-2, first);
-    put_addr(-1, second);
+  if (first_tile < n_tiles) {  // turn t - 2 brings K of tile t, turn t - 1 V of tile t and K of tile t + 1
+    const int t = first_tile;
+    int32_t first = page_of(t - 2), second = page_of(t - 1);
+    next = page_of(t);
+    put_addr(t - 2, first);
+    put_addr(t - 1, second);
     __syncthreads();
-    fetch_all(-2, 0, S::kLoads);
-    fetch_all(-1, 0, 2 * S::kLoads);
+    fetch_all(t - 2, 0, S::kLoads);
+    fetch_all(t - 1, 0, 2 * S::kLoads);
     landed();
     __syncthreads();
-    put_addr(0, settled(next));
-    next = page_of(1);
+    put_addr(t, settled(next));
+    next = page_of(t + 1);
   }
 
   const int k_row = (m32 & ~12) | (m32 & 4) << 1 | (m32 & 8) >> 1;
@@ -311,9 +343,9 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
     p[j] = round2<DT>(x, y);
   };
 
-  // Tiles this wave's rows see: the first w_tiles.
+  // Tiles this wave's rows see: those below w_tiles.
   int w_tiles = n_tiles;
-  while (w_tiles > 0) {
+  while (w_tiles > first_tile) {
     const int j0 = keys.key((w_tiles - 1) * BN);
     if (j0 <= wave_p1 || j0 < prefix) break;
     --w_tiles;
@@ -324,20 +356,21 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
   slope = settled(slope);
   f32x16 s[KT];
   float mx = -INFINITY;
-  if (w_tiles > 0) {
+  if (w_tiles > first_tile) {
+    const uint32_t place = k_base + (first_tile & 1) * S::kUnits * 16;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[kt][i] = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) s[i % KT] = mfma32x32<DT>(k_frag(k_base, i), q[i / KT], s[i % KT]);
+    for (int i = 0; i < kSteps; ++i) s[i % KT] = mfma32x32<DT>(k_frag(place, i), q[i / KT], s[i % KT]);
 #pragma unroll
-    for (int j = 0; j < kPairs; ++j) score_pair(0, s, j);
-    if (!all_seen(0, wg_p0, wg_p1)) mask(0, s);
+    for (int j = 0; j < kPairs; ++j) score_pair(first_tile, s, j);
+    if (!all_seen(first_tile, wg_p0, wg_p1)) mask(first_tile, s);
     mx = maximum(s);
   }
   bool cleared = false;  // some tile held an infinity or NaN
-  for (int t = 0; t < n_tiles; ++t) {
+  for (int t = first_tile; t < n_tiles; ++t) {
     landed();              // this wave's share of K of tile t + 1 and V of tile t
     next = settled(next);  // (waited for here, not behind the loads below)
     // A tile on some row's border. A weight of zero does not keep an infinity or NaN in V
@@ -447,7 +480,7 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
   if (cleared) {
     const int32_t* vt = a.vt + (int64_t)r * a.max_blocks;
 #pragma unroll 1
-    for (int i = 0; i < n_tiles * BN; ++i) {
+    for (int i = first_tile * BN; i < n_tiles * BN; ++i) {
       if (i % BN == 0 && all_seen(i / BN, wg_p0, wg_p1)) {
         i += BN - 1;
         continue;
@@ -472,6 +505,56 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
   }
 
   l = sum32(l);
+  if (rt.chunks > 1) {
+    // A chunk's result goes to the workspace as the lanes hold it, pairs of values 64 lanes
+    // wide, and the workgroup that finishes last adds the others' to its own. Parts are
+    // numbered 2 extra + chunk: a cut tile has at most twice its extra chunks.
+    float* const mine = a.part + (((int64_t)(2 * rt.extra) * a.hk + kv_head) * a.part_waves + wave) * part_floats(NC) + lane * 2;
+    const int64_t part_step = (int64_t)a.hk * a.part_waves * part_floats(NC);
+    const bool used = wave * kWaveRows < rows;  // (then wave < part_waves)
+    if (used) {
+      float* to = mine + rt.chunk * part_step;
+      put_pair(to, m, l);
+#pragma unroll
+      for (int d = 0; d < NC; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) put_pair(to + (1 + d * 8 + i / 2) * 128, acc[d][i], acc[d][i + 1]);
+    }
+    landed();
+    __syncthreads();
+    if (tid == 0) {
+      int32_t* counter = a.counters + rt.extra * a.hk + kv_head;
+      const int32_t done = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      sm_flag[0] = done == rt.chunks - 1;
+      if (done == rt.chunks - 1) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next call
+    }
+    __syncthreads();
+    if (!__builtin_amdgcn_readfirstlane(sm_flag[0]) || !used) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    // In the chunks' order, so that the result does not depend on which one was last.
+    float mt = -INFINITY;
+    for (int c = 0; c < rt.chunks; ++c) mt = fmaxf(mt, mine[c * part_step]);
+    m = mt;
+    l = 0.f;
+#pragma unroll
+    for (int d = 0; d < NC; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[d][i] = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < rt.chunks; ++c) {
+      const float* from = mine + c * part_step;
+      const float f = part_weight(from[0], mt);
+      l += f * from[1];
+#pragma unroll
+      for (int d = 0; d < NC; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+          const float2 x = *reinterpret_cast<const float2*>(from + (1 + d * 8 + i / 2) * 128);
+          acc[d][i] += f * x.x;
+          acc[d][i + 1] += f * x.y;
+        }
+    }
+  }
   if (my_row >= rows) return;
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   uint16_t* o = a.out + (int64_t)(q0 + tok) * a.o_ts + (int64_t)head * a.o_hs;
@@ -493,7 +576,7 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
 
 template <int DT, int MODE>
 hipError_t launch_mode(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev) {
-  const int64_t tiles = ((int64_t)a.n_tok * a.group + kTileM - 1) / kTileM + a.n_req;
+  const int64_t tiles = ((int64_t)a.n_tok * a.group + kTileM - 1) / kTileM + a.n_req + a.chunks;
   if (tiles * a.hk * kThreads >= kMaxThreads) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(tiles * a.hk));
   const int nc = (a.D + 31) / 32;

@@ -290,7 +290,9 @@ struct AttnArgs {
   // rows cut into chunks of their keys
   float* part;              // partial results
   int32_t* counters;        // finished chunks, all 0 between calls
-  int32_t chunks;           // decode: chunks to aim for, all requests together
+  int32_t chunks;           // decode: chunks to aim for, all requests together; prefill: past
+                            // one a row tile, at most (0: tiles stay whole)
+  int32_t part_waves;       // prefill: waves of a row tile that can hold rows
   int32_t wg_heads;         // decode: KV heads of a workgroup (1, 2 or 4)
 };
 // Floats of one row's partial result: max, sum, and the head's dimensions.
@@ -307,8 +309,23 @@ inline int32_t decode_units(int32_t n_req, int32_t hk, int32_t group) {
   return hk / decode_wg_heads(n_req, hk, group) * ((group + 15) / 16);
 }
 inline int32_t decode_chunks(int32_t units) { return (kDecodeTarget + units - 1) / units; }
-// The workspace begins with the counters: decode's are chunks aimed for x units, at most
-// kDecodeTarget + units, and hk + hq / 16 bounds units (hk <= 1024, hq <= 16384).
+// Prefill: one part's floats, of one wave (NC pieces of 32 dimensions of 32 rows, in pairs of
+// 64 lanes, and the pair m, l); instances of NC; chunks past one a row tile.
+constexpr int32_t part_floats(int32_t nc) { return 128 * (nc * 8 + 1); }
+inline int32_t attn_instance(int32_t D) {
+  const int32_t nc = (D + 31) / 32;
+  return nc <= 2 ? 2 : nc <= 4 ? nc : nc <= 6 ? 6 : 8;
+}
+inline int32_t prefill_chunks(int64_t n_tok, int32_t group, int32_t hk, int32_t max_len) {
+  const int64_t tiles = (n_tok * group + 127) / 128;
+  return max_len <= 512 || tiles * hk >= 2 * kDecodeTarget ? 0 : (kDecodeTarget + hk - 1) / hk;
+}
+inline int32_t prefill_waves(int64_t n_tok, int32_t group) {
+  return n_tok * group >= 128 ? 4 : (int32_t)((n_tok * group + 31) / 32);
+}
+// The workspace begins with the counters: chunks aimed for x units (decode) or x hk
+// (prefill), at most kDecodeTarget + units, and hk + hq / 16 bounds units (hk <= 1024, hq <=
+// 16384).
 constexpr int64_t kAttnCounters = kDecodeTarget + 2048;
 constexpr int64_t kAttnCounterBytes = kAttnCounters * 4;
 hipError_t launch_attn_decode(const AttnArgs& a, int32_t dtype, hipStream_t s, const LaunchEvents& ev);

@@ -155,6 +155,13 @@ int64_t decode_workspace(const slora_kv* kv, const slora_attn* at) {
                                  attn_part_floats(kv->head_dim) * (int64_t)sizeof(float);
 }
 
+int64_t prefill_workspace(const slora_kv* kv, const slora_attn* at, int32_t n_tokens) {
+  const int group = at->n_q_heads / kv->n_kv_heads;
+  const int64_t chunks = prefill_chunks(n_tokens, group, kv->n_kv_heads, kv->max_blocks * kv->tokens_per_page);
+  return kAttnCounterBytes + 2 * chunks * kv->n_kv_heads * prefill_waves(n_tokens, group) *
+                                 part_floats(attn_instance(kv->head_dim)) * (int64_t)sizeof(float);
+}
+
 int workspace_size(const slora_kv* kv, const slora_attn* at, int32_t n_tokens, int64_t* bytes) {
   const char* what = "attn_workspace_size";
   clear_error();
@@ -162,7 +169,7 @@ int workspace_size(const slora_kv* kv, const slora_attn* at, int32_t n_tokens, i
   if (n_tokens < 0) return fail(SLORA_E_INVALID, "%s: n_tokens %d < 0", what, n_tokens);
   const int rc = check_heads(what, kv, at);
   if (rc) return rc;
-  *bytes = n_tokens ? kAttnCounterBytes : decode_workspace(kv, at);
+  *bytes = n_tokens ? prefill_workspace(kv, at, n_tokens) : decode_workspace(kv, at);
   return SLORA_OK;
 }
 
@@ -248,9 +255,11 @@ int attn_prefill(const slora_kv* kv, const slora_attn* at, const int32_t* q_offs
   if (kv->n_requests == 0 || n_tokens == 0) return SLORA_OK;
   if (!q_offsets) return fail(SLORA_E_INVALID, "%s: q_offsets is NULL", what);
   AttnArgs a;
-  if ((rc = attn_args(what, kv, at, ws, ws_bytes, kAttnCounterBytes, &a))) return rc;
+  if ((rc = attn_args(what, kv, at, ws, ws_bytes, prefill_workspace(kv, at, n_tokens), &a))) return rc;
   a.q_offsets = q_offsets;
   a.n_tok = n_tokens;
+  a.chunks = prefill_chunks(n_tokens, a.group, a.hk, a.max_len);
+  a.part_waves = prefill_waves(n_tokens, a.group);
   const hipStream_t s = (hipStream_t)stream;
   const hipError_t e = timed_call(SLORA_K_ATTN_PREFILL, s,
                                   [&](const LaunchEvents& ev) { return launch_attn_prefill(a, kv->dtype, s, ev); });
