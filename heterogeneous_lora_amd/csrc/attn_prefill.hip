@@ -155,7 +155,7 @@ __device__ __forceinline__ uint2 read_turned(uint32_t at, int off) {
 enum Mode { kPlain, kCap, kAny };
 
 template <int DT, int NC, int MODE>
-__global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel(AttnArgs a) {
   using S = Shape<NC>;
   constexpr int BN = S::BN, KT = S::KT, CH = S::CH;
   __shared__ uint4 sm_k[2][S::kUnits];
@@ -284,6 +284,8 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
   // u). One xor and one addition make the address of a c's or d's; the rest is in the
   // instructions. (Kept in registers, the addresses would be spilled.)
   constexpr int kSteps = KT * NC * 2, kPairs = KT * 8, kRow = CH * 16;
+  // a step's share of the pairs of weights (or scores) and of the loads, at most
+  constexpr int kPairsStep = (kPairs + kSteps - 1) / kSteps, kLoadsStep = (2 * S::kLoads + kSteps - 1) / kSteps;
   const uint32_t k_base = lds_offset(sm_k) + k_row * kRow, k_xor = (h ^ S::k_swap(k_row)) * 16;
   const uint32_t v_base = lds_offset(sm_v) + v_key * kRow + v_c * 16 + v_in * 2, v_xor = S::v_swap(v_key) * 16;
   uint32_t frag_at = 0;
@@ -445,13 +447,19 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
       if (i + kAhead < kSteps) frag[i + kAhead] = k_frag(k_place, i + kAhead);
       else vfrag[i + kAhead - kSteps] = v_frag(v_place, i + kAhead - kSteps);
 #pragma unroll
-      for (int u = i * 2 * S::kLoads / kSteps; u < (i + 1) * 2 * S::kLoads / kSteps; ++u) {
-        fetch(t, u, row);
-        if (u + 1 < 2 * S::kLoads) row = row_of(t, u + 1);
+      for (int e = 0; e < kLoadsStep; ++e) {
+        const int u = i * 2 * S::kLoads / kSteps + e;
+        if (u < (i + 1) * 2 * S::kLoads / kSteps) {
+          fetch(t, u, row);
+          if (u + 1 < 2 * S::kLoads) row = row_of(t, u + 1);
+        }
       }
       sn[i % KT] = mfma32x32<DT>(frag[i], q[i / KT], sn[i % KT]);
 #pragma unroll
-      for (int j = i * kPairs / kSteps; j < (i + 1) * kPairs / kSteps; ++j) weight_pair(s, ms, p, j);
+      for (int e = 0; e < kPairsStep; ++e) {
+        const int j = i * kPairs / kSteps + e;
+        if (j < (i + 1) * kPairs / kSteps) weight_pair(s, ms, p, j);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
@@ -462,7 +470,10 @@ __global__ __launch_bounds__(kThreads, NC <= 4 ? 2 : 1) void attn_prefill_kernel
       const int b = i % (KT * 2) * 4, d = i / (KT * 2);
       acc[d] = mfma32x32<DT>(vfrag[i], make_uint4(p[b], p[b + 1], p[b + 2], p[b + 3]), acc[d]);
 #pragma unroll
-      for (int j = i * kPairs / kSteps; j < (i + 1) * kPairs / kSteps; ++j) score_pair(t + 1, sn, j);
+      for (int e = 0; e < kPairsStep; ++e) {
+        const int j = i * kPairs / kSteps + e;
+        if (j < (i + 1) * kPairs / kSteps) score_pair(t + 1, sn, j);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     // (the compiler would move the sum and the scores behind the branch)
