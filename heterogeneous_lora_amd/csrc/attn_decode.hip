@@ -45,7 +45,7 @@ __device__ __forceinline__ Seen seen_by(const AttnArgs& a, int32_t seq, int32_t 
   s.n = seq;
   s.bad = s.n < 0 || s.n > a.max_len;
   if (s.bad) s.n = 0;
-  s.keys = s.n > 0 ? keys_of(a, min(max(prefix, 0), s.n), s.n, s.n - 1, s.n - 1) : Keys{0, 0, 0};
+  s.keys = s.n > 0 ? keys_of(a, min(max(prefix, 0), s.n), s.n, s.n - 1, s.n - 1, 1) : Keys{0, 0, 0};
   return s;
 }
 

@@ -58,12 +58,14 @@ struct Keys {
 };
 
 // For rows at positions p_min .. p_max of a request with n cached keys (p_max < n) and a
-// prefix of 0 .. n.
-__device__ __forceinline__ Keys keys_of(const AttnArgs& a, int32_t prefix, int32_t n, int32_t p_min, int32_t p_max) {
+// prefix of 0 .. n. The hole behind the prefix begins at a multiple of `unit` (above 1: the
+// run then has keys that no row sees).
+__device__ __forceinline__ Keys keys_of(const AttnArgs& a, int32_t prefix, int32_t n, int32_t p_min, int32_t p_max,
+                                        int32_t unit) {
   const int32_t lo = a.window ? max(p_min - a.window + 1, 0) : 0;
   const int32_t end = max(p_max + 1, prefix);
   Keys k;
-  k.pre = min(prefix, lo);
+  k.pre = min((prefix + unit - 1) / unit * unit, lo);
   k.gap = lo - k.pre;
   if (lo >= end) {  // nothing past the prefix
     k.gap = 0;

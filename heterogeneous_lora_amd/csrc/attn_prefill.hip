@@ -150,9 +150,9 @@ __device__ __forceinline__ uint2 read_turned(uint32_t at, int off) {
 }
 
 // What a score passes through between the two products. kPlain: the scale alone, taken in
-// the subtraction of the maximum. kCap: softcap. kAny: a bias that depends on distance, with
-// or without softcap, and scales of zero or below (which would turn a masked -infinity).
-enum Mode { kPlain, kCap, kAny };
+// the subtraction of the maximum. kCap: softcap. kBias, kBiasCap: a bias that depends on
+// distance after them, and scales of zero or below (which would turn a masked -infinity).
+enum Mode { kPlain, kCap, kBias, kBiasCap };
 
 template <int DT, int NC, int MODE>
 __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel(AttnArgs a) {
@@ -186,7 +186,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
   const int head = kv_head * a.group + head0 + min(my_row, rows - 1) - (tok - tok0) * a.group;
   const int wave_p0 = pos_of(wave * kWaveRows), wave_p1 = pos_of(wave * kWaveRows + kWaveRows - 1);
   const int wg_p0 = first_pos + tok0, wg_p1 = pos_of(kTileM - 1);
-  const Keys keys = n > 0 ? keys_of(a, prefix, n, wg_p0, wg_p1) : Keys{0, 0, 0};
+  const Keys keys = n > 0 ? keys_of(a, prefix, n, wg_p0, wg_p1, BN) : Keys{0, 0, 0};
   // this chunk's tiles of keys
   const int all_tiles = (keys.count + BN - 1) / BN, per_chunk = (all_tiles + rt.chunks - 1) / rt.chunks;
   const int first_tile = min(rt.chunk * per_chunk, all_tiles), n_tiles = min(first_tile + per_chunk, all_tiles);
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
       q[c] = ld16(d < a.D ? qp + d : kAttnFill.zero);
     }
   }
-  float slope = MODE == kAny && a.slopes ? a.slopes[head] * kLog2e : 0.f;
+  float slope = MODE >= kBias && a.slopes ? a.slopes[head] * kLog2e : 0.f;
   // Scores are s * mul, or s * mul + cap: with softcap s is the reciprocal 1 / (e^(2 x / cap) +
   // 1) in cap tanh(x / cap) = cap - 2 cap s.
   const float mul = MODE == kPlain ? a.scale2 : MODE == kCap ? -2.0f * a.cap_out : 1.f;
@@ -301,21 +301,21 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
   };
   // Scores 2 j and 2 j + 1 of a lane, from the products. Register i of product kt: index t *
   // BN + kt * 32 + 16 (i / 8) + 8 h + i % 8 of the run.
-  auto score_pair = [&](int t, f32x16 (&s)[KT], int j) {
+  auto score_pair = [&](float far, f32x16 (&s)[KT], int j) {  // far: of register 0, key - position
     const int kt = j / 8;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int i = j % 8 * 2 + e;
       float x = s[kt][i];
       if (MODE == kCap) x = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * a.cap_in) + 1.0f);
-      else if (MODE == kAny) x = a.cap_out != 0.f ? capped(a, x) : x * a.scale2;
-      if (MODE == kAny) {
-        const int k = kt * 32 + 16 * (i / 8) + i % 8, at = t * BN + 8 * h;
-        x += slope * (float)((k >= keys.pre - at ? keys.gap : 0) + at - pos + k);
-      }
+      else if (MODE == kBiasCap) x = capped(a, x);
+      else if (MODE == kBias) x *= a.scale2;
+      if (MODE >= kBias) x = __builtin_fmaf(slope, far + (float)(kt * 32 + 16 * (i / 8) + i % 8), x);
       s[kt][i] = x;
     }
   };
+  // (a tile lies on one side of the hole behind the prefix)
+  auto far_of = [&](int t) { return MODE >= kBias ? (float)(keys.key(t * BN) + 8 * h - pos) : 0.f; };
   // -infinity for what the row must not see of a border tile.
   auto mask = [&](int t, f32x16 (&s)[KT]) {
     const int at = t * BN + 8 * h, hi = see_hi - at, lo = see_lo - at, pre = prefix - at;
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) s[i % KT] = mfma32x32<DT>(k_frag(place, i), q[i / KT], s[i % KT]);
 #pragma unroll
-    for (int j = 0; j < kPairs; ++j) score_pair(first_tile, s, j);
+    for (int j = 0; j < kPairs; ++j) score_pair(far_of(first_tile), s, j);
     if (!all_seen(first_tile, wg_p0, wg_p1)) mask(first_tile, s);
     mx = maximum(s);
   }
@@ -431,6 +431,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
     uint32_t p[KT * 8];
     const float ms = (MODE == kCap ? a.cap_out : 0.f) - (m == -INFINITY ? 0.f : m);
     const bool edge_next = !all_seen(t + 1, wg_p0, wg_p1);
+    const float far = far_of(t + 1);
     const uint32_t k_place = k_base + ((t + 1) & 1) * S::kUnits * 16, v_place = v_base + (t & 1) * S::kUnits * 16;
     uint4 frag[kSteps];
 #pragma unroll
@@ -472,7 +473,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
 #pragma unroll
       for (int e = 0; e < kPairsStep; ++e) {
         const int j = i * kPairs / kSteps + e;
-        if (j < (i + 1) * kPairs / kSteps) score_pair(t + 1, sn, j);
+        if (j < (i + 1) * kPairs / kSteps) score_pair(far, sn, j);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -604,9 +605,11 @@ hipError_t launch_mode(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev)
 
 template <int DT>
 hipError_t launch_dt(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev) {
-  return a.slopes || !(a.scale2 > 0.f) ? launch_mode<DT, kAny>(a, s, ev)
-         : a.cap_out != 0.f           ? launch_mode<DT, kCap>(a, s, ev)
-                                      : launch_mode<DT, kPlain>(a, s, ev);
+  const bool cap = a.cap_out != 0.f, bias = a.slopes || !(a.scale2 > 0.f);
+  return bias && cap ? launch_mode<DT, kBiasCap>(a, s, ev)
+         : bias      ? launch_mode<DT, kBias>(a, s, ev)
+         : cap       ? launch_mode<DT, kCap>(a, s, ev)
+                     : launch_mode<DT, kPlain>(a, s, ev);
 }
 
 }  // namespace
