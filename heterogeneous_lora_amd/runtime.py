@@ -234,6 +234,11 @@ class ServingLoop:
     def step(self, seed: int):
         """Plan one step, fetch what it needs, run its batch. Returns (batch dict, x, y0, y)
         as host arrays (uint16 bits) for checking, or the batch alone when it is empty."""
+        b, x, y0, yd = self._project(seed)
+        return b, x, y0, None if yd is None else yd.cpu().numpy().view(np.uint16)
+
+    def _project(self, seed: int):
+        """step(), with y left on the device."""
         b = self.sched.step()
         if b["fetch"].size:
             done = torch.cuda.Event()
@@ -270,7 +275,7 @@ class ServingLoop:
         if status:
             raise RuntimeError(f"step {b['step']}: a decode launch gave up waiting")
         self.steps_run += 1
-        return b, x, y0, yd.cpu().numpy().view(np.uint16)
+        return b, x, y0, yd
 
     def close(self):
         torch.cuda.synchronize(self.device)
@@ -476,3 +481,72 @@ class KVCache:
         call()
         if stream is not None:  # a workspace made here goes back to its own stream's memory
             call.tensors[-1].record_stream(stream)
+
+
+class AttentionLoop(ServingLoop):
+    """ServingLoop whose projection makes a layer's packed q, k and v: every step's new
+    tokens are normalised, rotated and stored to the KV pages that the scheduler took from
+    the unified pool for them, new prompts attend over themselves (slora_attn_prefill) and
+    running requests' new tokens over their caches (slora_attn_decode).
+
+    d_out of the projection is (n_q_heads + 2 n_kv_heads) * head_dim; max_len bounds a
+    request's tokens. attention: softcap, window, slopes, scale as KVCache.bind_decode takes
+    them; write: norm, q_weight, k_weight, eps as KVCache.bind_write does."""
+
+    def __init__(self, wl, n_pages: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_len: int,
+                 rope: Optional[Rope] = None, attention: Optional[dict] = None, write: Optional[dict] = None, **kw):
+        super().__init__(wl, n_pages, kv_pages_per_token=2, **kw)  # a K page and a V page a token
+        if self.d_out != (n_q_heads + 2 * n_kv_heads) * head_dim:
+            raise ValueError(f"d_out {self.d_out} is not {n_q_heads} + 2 x {n_kv_heads} heads of {head_dim}")
+        self.n_q_heads, self.n_kv_heads, self.head_dim, self.max_len = n_q_heads, n_kv_heads, head_dim, max_len
+        self.cache = KVCache(self.pool_t, n_pages, page_elems=wl.page_elems, dtype=wl.dtype,
+                             n_kv_heads=n_kv_heads, head_dim=head_dim, tokens_per_page=1)
+        self.rope, self.attention, self.write_options = rope, attention or {}, write or {}
+        self.cached: Dict[int, int] = {}  # tokens of each running request in the cache
+        self.ws: Optional[torch.Tensor] = None
+
+    def _workspace(self, calls) -> torch.Tensor:
+        """One workspace for every call of the loop, grown as steps need it. calls: (requests,
+        prompt tokens) of each, 0 tokens for slora_attn_decode."""
+        a = _lib.Attn(n_q_heads=self.n_q_heads)
+        need = max(_lib.attn_workspace_size(self.cache._kv(r, self.max_len), a, n) for r, n in calls)
+        if self.ws is None or self.ws.numel() < need:
+            self.ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        return self.ws
+
+    def step(self, seed: int):
+        """One step. Returns (batch dict, qkv, out) with the projections [tokens, heads, head_dim]
+        (queries, keys, values) and the attention's output [tokens, n_q_heads, head_dim] on the
+        device, in the batch's order: new prompts' tokens, then one of each running request."""
+        b, _, _, y = self._project(seed)
+        gone = [int(r) for r in np.concatenate([b["finished"], b["aborted"]])]
+        for r in gone:
+            self.cached.pop(r, None)
+        if y is None:
+            return b, None, None
+        prompts, running = [int(r) for r in b["seg_request"]], [int(r) for r in b["token_request"]]
+        new = np.concatenate([np.diff(b["seg_offsets"]), np.ones(len(running), np.int32)]).astype(np.int32)
+        requests = prompts + running
+        past = np.array([self.cached.get(r, 0) for r in requests], np.int32)
+        if int((past + new).max()) > self.max_len:
+            raise ValueError(f"a request passes {self.max_len} tokens")
+        dev = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(self.device)
+        pages = np.concatenate([self.sched.request_pages(r) for r in requests])
+        T, S, first = b["n_tokens"], len(prompts), int(b["seg_offsets"][-1])
+        t = KVTables(2, len(requests), self.max_len, T, device=self.device)
+        self.cache.tables(t, dev(pages), dev(past), dev(new))
+        hq, hk = self.n_q_heads, self.n_kv_heads
+        qkv = y.view(TORCH_DTYPES[self.wl.dtype]).view(T, hq + 2 * hk, self.head_dim)
+        q, k, v = qkv.split([hq, hk, hk], dim=1)
+        rotated, out = (torch.empty(T, hq, self.head_dim, dtype=qkv.dtype, device=self.device) for _ in range(2))
+        self.cache.write(q, k, v, rotated, t.position, t.slots[0], t.slots[1], rope=self.rope, **self.write_options)
+        ws = self._workspace([(S, first), (len(running), 0)])
+        if S:
+            self.cache.prefill(rotated[:first], out[:first], t.table[0, :S], t.table[1, :S], t.seq_len[:S],
+                               t.q_offsets[:S + 1], ws=ws, **self.attention)
+        if running:
+            self.cache.decode(rotated[first:], out[first:], t.table[0, S:], t.table[1, S:], t.seq_len[S:],
+                              ws=ws, **self.attention)
+        for r, n in zip(requests, past + new):
+            self.cached[r] = int(n)
+        return b, qkv, out
