@@ -69,11 +69,18 @@ __device__ Sums sums_before(const slora_kv_step& st, int32_t tpp, int r) {
   return s;
 }
 
+// A value that is the same on every thread, in scalar registers.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)x >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // Lanes that take one row of n elements: a power of two up to 64.
 __device__ __forceinline__ int row_lanes_log2(int n) { return n >= 64 ? 6 : n <= 1 ? 0 : 32 - __builtin_clz(n - 1); }
 
 // blockIdx.y = request (n_requests: the rows past the step's tokens), blockIdx.x = its
 // share of the row's tiles, blockIdx.z = group of planes.
+template <bool APPEND>
 __global__ __launch_bounds__(kThreads) void kv_tables_kernel(slora_kv_step st, int64_t n_pages, int32_t tpp, int32_t n_req,
                                                              int32_t max_blocks, int32_t group, uint32_t magic,
                                                              uint32_t shift) {
@@ -98,14 +105,14 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(slora_kv_step st, i
 
   const Request q = request(st, tpp, r);
   // blocks this row deals with: all of it, or the ones the new tokens touch
-  const int64_t b_begin = st.append ? q.past / tpp : 0;
-  const int64_t b_used = q.seq > q.past || !st.append ? min(q.blocks, (int64_t)max_blocks) : b_begin;
-  const int64_t b_end = st.append ? b_used : max_blocks;
+  const int64_t b_begin = APPEND ? q.past / tpp : 0;
+  const int64_t b_used = q.seq > q.past || !APPEND ? min(q.blocks, (int64_t)max_blocks) : b_begin;
+  const int64_t b_end = APPEND ? b_used : max_blocks;
   const int stride = np | 1;
   const int64_t tile0 = b_begin + (int64_t)sub * kBlocks;
   if (sub != 0 && tile0 >= b_end) return;
   // 16-byte stores where the rows allow them (a tile begins at a multiple of 64 blocks)
-  const bool wide = !st.append && max_blocks % 4 == 0 && ((uintptr_t)st.tables & 15) == 0;
+  const bool wide = !APPEND && max_blocks % 4 == 0 && ((uintptr_t)st.tables & 15) == 0;
 
   // Rows past the request's blocks are -1 and need no sums.
   const bool any_used = sub == 0 || tile0 < b_used;
@@ -117,25 +124,54 @@ __global__ __launch_bounds__(kThreads) void kv_tables_kernel(slora_kv_step st, i
     st.q_offsets[r] = (int32_t)min(t_first, T);
   }
 
+  // A tile's page ids: entry i is block i / group's id of plane i % group.
+  const int64_t list0 = uniform(before.blocks) - q.first;
+  auto block_of = [&](int i) { return group == 1 ? i : (int)(__umulhi((uint32_t)i, magic) >> shift); };
+  auto used_from = [&](int64_t b0) { return (int)max(min(min(b0 + kBlocks, b_end), b_used) - b0, (int64_t)0); };
+  // A rebuild reads them a tile ahead of the rows being written, kHold to a thread, all
+  // loads in flight at once (an id past the tile or the list reads the last one).
+  constexpr int kHold = kBlocks * kPlanes / kThreads;
+  int32_t held[kHold];
+  auto read = [&](int64_t b0) {
+    const int n_used = used_from(b0);
+    const int64_t at0 = (list0 + b0) * st.n_planes + p0, left = st.n_page_ids - at0;
+    if (n_used == 0 || left <= 0) return;
+    const int last = (int)min((int64_t)((n_used - 1) * st.n_planes + np), left) - 1;
+    const int32_t* from = st.pages + at0;
+#pragma unroll
+    for (int u = 0; u < kHold; ++u) {
+      const int i = tid + u * kThreads, b = block_of(i);
+      held[u] = from[min(b * st.n_planes + i - b * group, last)];
+    }
+  };
+  if (!APPEND) read(tile0);
   for (int64_t b0 = tile0; b0 < b_end; b0 += (int64_t)n_sub * kBlocks) {
-    const int64_t b1 = min(b0 + kBlocks, b_end);
-    const int n = (int)(b1 - b0), n_used = (int)max(min(b1, b_used) - b0, (int64_t)0);
+    const int n = (int)(min(b0 + kBlocks, b_end) - b0), n_used = used_from(b0);
     if (n_used > 0) {
+      const int64_t at0 = (list0 + b0) * st.n_planes + p0, left = st.n_page_ids - at0;
       __syncthreads();  // the previous tile has been read
-      const int64_t at0 = (before.blocks + b0 - q.first) * st.n_planes + p0;
-      for (int i = tid; i < n_used * group; i += kThreads) {
-        const int b = group == 1 ? i : (int)(__umulhi((uint32_t)i, magic) >> shift), p = i - b * group;
-        if (p >= np) continue;
-        int32_t page = -1;
-        if (b0 + b >= q.first) {
-          const int64_t at = at0 + (int64_t)b * st.n_planes + p;
-          if (at < st.n_page_ids) page = st.pages[at];
-        } else {  // append: the block the step before left part full
-          page = st.tables[((int64_t)(p0 + p) * n_req + r) * max_blocks + b0 + b];
+      if (APPEND) {
+        for (int i = tid; i < n_used * group; i += kThreads) {
+          const int b = block_of(i), p = i - b * group;
+          if (p >= np) continue;
+          int32_t page = -1;
+          if (b0 + b >= q.first) {
+            const int64_t off = (int64_t)b * st.n_planes + p;
+            if (off < left) page = st.pages[at0 + off];
+          } else {  // the block the step before left part full
+            page = st.tables[((int64_t)(p0 + p) * n_req + r) * max_blocks + b0 + b];
+          }
+          tile[b * stride + p] = page;
         }
-        tile[b * stride + p] = page;
+      } else {
+#pragma unroll
+        for (int u = 0; u < kHold; ++u) {
+          const int i = tid + u * kThreads, b = block_of(i), p = i - b * group;
+          if (b < n_used && p < np) tile[b * stride + p] = (int64_t)b * st.n_planes + p < left ? held[u] : -1;
+        }
       }
       __syncthreads();
+      if (!APPEND) read(b0 + (int64_t)n_sub * kBlocks);
     }
     // table rows: from the tile, -1 past the request's blocks
     if (wide) {
@@ -209,9 +245,10 @@ hipError_t launch_kv_tables(const slora_kv& kv, const slora_kv_step& st, hipStre
   const int64_t tiles = (blocks + kBlocks - 1) / kBlocks;
   if (sub > tiles) sub = tiles;
   if (sub < 1) sub = 1;
-  hipExtLaunchKernelGGL(kv_tables_kernel, dim3((unsigned)sub, (unsigned)(kv.n_requests + 1), (unsigned)groups),
-                        dim3(kThreads), 0, s, ev.start, ev.stop, 0, st, kv.n_pages, kv.tokens_per_page,
-                        kv.n_requests, kv.max_blocks, group, magic, shift);
+  hipExtLaunchKernelGGL(st.append ? kv_tables_kernel<true> : kv_tables_kernel<false>,
+                        dim3((unsigned)sub, (unsigned)(kv.n_requests + 1), (unsigned)groups), dim3(kThreads), 0, s,
+                        ev.start, ev.stop, 0, st, kv.n_pages, kv.tokens_per_page, kv.n_requests, kv.max_blocks, group,
+                        magic, shift);
   return hipGetLastError();
 }
 
