@@ -59,46 +59,45 @@ struct Place {
 };
 
 // The number nearest to count / chunk: one key more does not make a chunk of its own.
-__device__ __forceinline__ int chunks_of(int32_t count, int32_t chunk) {
-  return count <= chunk ? 1 : (int)(((uint32_t)count + (uint32_t)chunk / 2) / (uint32_t)chunk);
+__device__ __forceinline__ int chunks_of(int32_t count, float per_chunk) {
+  return max((int)((float)count * per_chunk + 0.5f), 1);
 }
 
 // The request whose chunks hold number x. A chunk is all requests' keys spread over the
-// workgroups aimed for, in whole rounds; every wave of the call finds the same. A lane
-// takes kHold requests at a time, all their loads in flight at once, and keeps them where
+// workgroups aimed for, in whole rounds of keys; every wave of the call finds the same. A
+// lane takes HOLD requests at a time, all their loads in flight at once, and keeps them where
 // one turn covers the call: each turn is one memory latency that nothing hides.
-constexpr int kHold = 8, kTurn = 64 * kHold;
+template <int HOLD>
 __device__ __forceinline__ Place find_chunk(const AttnArgs& a, int lane, int x, int round) {
-  int32_t seq[kHold], prefix[kHold], count[kHold];
+  constexpr int kTurn = 64 * HOLD;
+  int32_t seq[HOLD], prefix[HOLD], count[HOLD];
   auto load = [&](int r0) {
 #pragma unroll
-    for (int k = 0; k < kHold; ++k) {
-      const int r = min(r0 + lane * kHold + k, a.n_req - 1);
+    for (int k = 0; k < HOLD; ++k) {
+      const int r = min(r0 + lane * HOLD + k, a.n_req - 1);
       seq[k] = a.seq[r];
       prefix[k] = a.prefix ? a.prefix[r] : 0;
     }
 #pragma unroll
-    for (int k = 0; k < kHold; ++k)
-      count[k] = r0 + lane * kHold + k < a.n_req ? seen_by(a, seq[k], prefix[k]).keys.count : -1;
+    for (int k = 0; k < HOLD; ++k)
+      count[k] = r0 + lane * HOLD + k < a.n_req ? seen_by(a, seq[k], prefix[k]).keys.count : -1;
   };
   float total = 0.f;
   for (int r0 = 0; r0 < a.n_req; r0 += kTurn) {
     load(r0);
 #pragma unroll
-    for (int k = 0; k < kHold; ++k) total += (float)max(count[k], 0);
+    for (int k = 0; k < HOLD; ++k) total += (float)max(count[k], 0);
   }
   // (In 32 bits the keys may be off by a part in 10^6: the chunks past one a request stay a
   // whole number not above a.chunks, which is what the workspace is sized for.)
-  const float want = wave_sum(total) / (float)a.chunks;
-  const int32_t rounds = want < 1e9f ? (int32_t)want / round + 1 : (1 << 30) / round;
-  const int32_t chunk = rounds * round;
+  const float per_chunk = 1.0f / fmaxf(wave_sum(total) / (float)a.chunks + (float)round, 1.f);
 
   int before = 0;
   for (int r0 = 0; r0 < a.n_req; r0 += kTurn) {
     if (a.n_req > kTurn) load(r0);
     int mine = 0;
 #pragma unroll
-    for (int k = 0; k < kHold; ++k) mine += count[k] < 0 ? 0 : chunks_of(count[k], chunk);
+    for (int k = 0; k < HOLD; ++k) mine += count[k] < 0 ? 0 : chunks_of(count[k], per_chunk);
     const int sum = running_sum(mine);
     const uint64_t hit = __ballot(x < before + sum);
     if (hit) {
@@ -106,10 +105,10 @@ __device__ __forceinline__ Place find_chunk(const AttnArgs& a, int lane, int x, 
       Place p{-1, before + sum - mine, 0, 0, 0};
       bool found = false;
 #pragma unroll
-      for (int k = 0; k < kHold; ++k) {  // lane l's requests; the other lanes' result is not read
-        const int c = count[k] < 0 ? 0 : chunks_of(count[k], chunk);
+      for (int k = 0; k < HOLD; ++k) {  // lane l's requests; the other lanes' result is not read
+        const int c = count[k] < 0 ? 0 : chunks_of(count[k], per_chunk);
         if (!found && x < p.first + c) {
-          p.r = r0 + lane * kHold + k;
+          p.r = r0 + lane * HOLD + k;
           p.n = c;
           p.seq = seq[k];
           p.prefix = prefix[k];
@@ -162,22 +161,24 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m16 = lane & 15, g = lane >> 4;
   // a workgroup: `heads` neighbouring KV heads, `phases` waves on each
-  const int heads = a.wg_heads, phases = kWaves / heads, phase = wave / heads;
-  const int round = phases * kTile;
+  const int heads_log2 = a.wg_heads >> 1, heads = a.wg_heads;  // 1, 2, 4: 0, 1, 2
+  const int phases = kWaves >> heads_log2, phase = wave >> heads_log2, my_head = wave & (heads - 1);
+  const int round_log2 = 7 - heads_log2, round = 1 << round_log2;  // phases * kTile
   const int row_groups = (a.group + kRows - 1) / kRows;
-  const int units = a.hk / heads * row_groups;
-  const int unit = (int)(blockIdx.x % (uint32_t)units), x_chunk = (int)(blockIdx.x / (uint32_t)units);
-  const Place at = find_chunk(a, lane, x_chunk, round);
+  const int units = (int)gridDim.x, unit = (int)blockIdx.x, x_chunk = (int)blockIdx.y;
+  const Place at = a.n_req <= 64 ? find_chunk<1>(a, lane, x_chunk, round) : find_chunk<8>(a, lane, x_chunk, round);
   if (at.r < 0) return;
   const int r = at.r;
   const Seen seen = seen_by(a, at.seq, at.prefix);
-  const int kv_head = unit / row_groups * heads + wave % heads, row0 = (unit % row_groups) * kRows;
+  const int head_unit = row_groups == 1 ? unit : unit / row_groups;
+  const int kv_head = (head_unit << heads_log2) + my_head, row0 = (unit - head_unit * row_groups) * kRows;
   const int rows = min(a.group - row0, kRows);
   const int head0 = kv_head * a.group + row0;
   const int h_off = kv_head * a.D;
   // its chunks are of one length, in whole rounds (the last ones may be empty)
   const int32_t count = seen.keys.count;
-  const int32_t length = ((uint32_t)(count + at.n - 1) / (uint32_t)at.n + round - 1) / (uint32_t)round * round;
+  const int32_t each = at.n == 1 ? count : (int32_t)((uint32_t)(count + at.n - 1) / (uint32_t)at.n);
+  const int32_t length = (each + round - 1) >> round_log2 << round_log2;
   const int begin = min((x_chunk - at.first) * length, count), end = min(begin + length, count);
 
   // q, as the B operand: lane l holds dimensions 32 c + 8 (l / 16) .. + 7 of row l % 16
@@ -199,7 +200,7 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
     for (int e = 0; e < VD; ++e) acc[h][e] = {0.f, 0.f, 0.f, 0.f};
   float m = -INFINITY, l = 0.f;
 
-  const int n_tiles = end > begin + phase * kTile ? (int)((uint32_t)(end - begin - phase * kTile + round - 1) / (uint32_t)round) : 0;
+  const int n_tiles = end > begin + phase * kTile ? (end - begin - phase * kTile + round - 1) >> round_log2 : 0;
   // lane l looks up key l % 32 of the tile: its K page (l < 32) or V page
   const int32_t* table = (lane < 32 ? a.kt : a.vt) + (int64_t)r * a.max_blocks;
   auto tile_begin = [&](int t) { return begin + phase * kTile + t * round; };
@@ -391,7 +392,7 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
       x += f * o.x;
       y += f * o.y;
     }
-    const int hq = (unit / row_groups * heads + hw) * a.group + row0 + row;
+    const int hq = ((head_unit << heads_log2) + hw) * a.group + row0 + row;
     if (at.n == 1) {
       const float inv = lt == 0.f ? 0.f : 1.0f / lt;
       *reinterpret_cast<uint32_t*>(a.out + (int64_t)r * a.o_ts + (int64_t)hq * a.o_hs + d) =
@@ -418,7 +419,7 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
   if (!__builtin_amdgcn_readfirstlane(sm_last)) return;
   // rows of all the workgroup's heads, a wave to each in turn
   for (int i = wave; i < heads * rows; i += kWaves) {
-    const int hq = (unit / row_groups * heads + i / rows) * a.group + row0 + i % rows;
+    const int hq = ((head_unit << heads_log2) + i / rows) * a.group + row0 + i % rows;
     const float* part = a.part + (int64_t)at.first * part_chunk + hq * part_row;
     float mt = -INFINITY;
     for (int c = lane; c < at.n; c += 64) mt = fmaxf(mt, get_part(part + c * part_chunk));
@@ -463,7 +464,7 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
 }
 
 template <int DT, int NC>
-hipError_t launch_nc(const AttnArgs& a, unsigned grid, hipStream_t s, const LaunchEvents& ev) {
+hipError_t launch_nc(const AttnArgs& a, dim3 grid, hipStream_t s, const LaunchEvents& ev) {
   const int rows = a.group < kRows ? a.group : kRows;
   const size_t lds = sizeof(float) * kWaves * rows * (a.D + 4);
   if (lds > 48 * 1024) {  // with the static part past the 64 KiB a launch has by default
@@ -471,7 +472,7 @@ hipError_t launch_nc(const AttnArgs& a, unsigned grid, hipStream_t s, const Laun
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipExtLaunchKernelGGL((attn_decode_kernel<DT, NC>), dim3(grid), dim3(kWaves * 64), lds, s, ev.start, ev.stop, 0, a);
+  hipExtLaunchKernelGGL((attn_decode_kernel<DT, NC>), grid, dim3(kWaves * 64), lds, s, ev.start, ev.stop, 0, a);
   return hipGetLastError();
 }
 
@@ -483,7 +484,7 @@ hipError_t launch_dt(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev) {
   const int64_t most = (a.max_len + round - 1) / round, all = (int64_t)a.n_req * (most > 1 ? most : 1);
   const int64_t chunks = all < (int64_t)a.n_req + a.chunks ? all : (int64_t)a.n_req + a.chunks;
   if (chunks * units * kWaves * 64 >= kMaxThreads) return hipErrorInvalidConfiguration;
-  const unsigned grid = (unsigned)(chunks * units);
+  const dim3 grid((unsigned)units, (unsigned)chunks);  // neighbouring heads in neighbouring workgroups
   const int nc = (a.D + 31) / 32;
   return nc <= 2   ? launch_nc<DT, 2>(a, grid, s, ev)
          : nc == 3 ? launch_nc<DT, 3>(a, grid, s, ev)

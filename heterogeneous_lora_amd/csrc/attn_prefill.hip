@@ -104,7 +104,7 @@ __device__ __forceinline__ RowTile find_tile(const AttnArgs& a, int lane, int x)
     if (hit) {
       const int l = __builtin_ctzll(hit);
       auto of = [&](int v) { return __builtin_amdgcn_readlane(v, l); };
-      const int c = of(chunks), i = x - before - of(sum - mine), t = i / c;
+      const int c = of(chunks), i = x - before - of(sum - mine), t = c == 1 ? i : i / c;
       // later tiles of a request see more keys: they go first
       return {r0 + l, of(tiles) - 1 - t, i - t * c, c, extra + of(extra_sum - extra_mine) + t * (c - 1),
               of(q0), of(n_new), of(n), of(prefix)};
@@ -175,8 +175,9 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
 
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int m32 = lane & 31, h = lane >> 5;
-  const int kv_head = (int)(blockIdx.x % (uint32_t)a.hk);
-  const RowTile rt = find_tile(a, lane, (int)(blockIdx.x / (uint32_t)a.hk));
+  const int tile_x = a.hk == 1 ? (int)blockIdx.x : (int)(__umulhi(blockIdx.x, a.hk_magic) >> a.hk_shift);
+  const int kv_head = (int)blockIdx.x - tile_x * a.hk;
+  const RowTile rt = find_tile(a, lane, tile_x);
   const int r = rt.r, row_tile = rt.tile, q0 = rt.q0, n_new = rt.n_new;
   if (r < 0) return;
   const bool bad = rt.n < 0 || rt.n > a.max_len;
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
 
   // Row i of the tile: token tok0 + (head0 + i) / group, query head (head0 + i) % group.
   const int rows = (int)min((int64_t)n_new * a.group - (int64_t)row_tile * kTileM, (int64_t)kTileM);
-  const int tile_q = row_tile / a.group, tile_r = row_tile - tile_q * a.group;
+  const int tile_q = (int)div_group(a, (uint32_t)row_tile), tile_r = row_tile - tile_q * a.group;
   const int tok0 = tile_q * kTileM + (int)div_group(a, (uint32_t)(tile_r * kTileM));
   const int head0 = tile_r * kTileM - (tok0 - tile_q * kTileM) * a.group;
   auto pos_of = [&](int i) { return first_pos + tok0 + (int)div_group(a, (uint32_t)(head0 + min(i, rows - 1))); };
@@ -198,7 +199,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
   const int wg_p0 = first_pos + tok0, wg_p1 = pos_of(kTileM - 1);
   const Keys keys = n > 0 ? keys_of(a, prefix, n, wg_p0, wg_p1, BN) : Keys{0, 0, 0};
   // this chunk's tiles of keys
-  const int all_tiles = (keys.count + BN - 1) / BN, per_chunk = (all_tiles + rt.chunks - 1) / rt.chunks;
+  const int all_tiles = (keys.count + BN - 1) / BN, per_chunk = rt.chunks == 1 ? all_tiles : (all_tiles + rt.chunks - 1) / rt.chunks;
   const int first_tile = min(rt.chunk * per_chunk, all_tiles), n_tiles = min(first_tile + per_chunk, all_tiles);
   const int h_off = kv_head * a.D;
   // In terms of the run's indices the row sees [0, prefix) and [see_lo, see_hi].

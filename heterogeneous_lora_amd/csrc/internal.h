@@ -270,7 +270,8 @@ struct AttnArgs {
   uint32_t n_pages_u;       // page ids below it are in the pool (as unsigned: -1 is not)
   int32_t P, tpp;
   uint32_t tpp_magic, tpp_shift;  // n / tpp = umulhi(n, magic) >> shift for n < 2^31, tpp > 1
-  uint32_t group_magic, group_shift;  // the same for group
+  uint32_t group_magic, group_shift;  // the same for group, and for hk
+  uint32_t hk_magic, hk_shift;
   int32_t row;              // n_kv_heads * head_dim
   int32_t n_req, max_blocks, hk, group, D;
   int32_t max_len;          // max_blocks * tpp

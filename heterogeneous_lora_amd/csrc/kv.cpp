@@ -196,6 +196,7 @@ int attn_args(const char* what, const slora_kv* kv, const slora_attn* at, void* 
   a->tpp = kv->tokens_per_page;
   divisor(a->tpp, &a->tpp_magic, &a->tpp_shift);
   a->hk = kv->n_kv_heads;
+  divisor(a->hk, &a->hk_magic, &a->hk_shift);
   a->D = kv->head_dim;
   a->row = a->hk * a->D;
   a->n_req = kv->n_requests;
