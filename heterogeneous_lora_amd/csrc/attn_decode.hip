@@ -14,7 +14,7 @@
 // depend on which one that is.
 //
 // 512 requests of 64 to 2048 keys, 40 heads of 128: 1.89 ms (5.9 TB/s); three of 100000 to
-// 131072 keys, 64 query heads on 8: 270 us (5.3 TB/s); 64 with a window of 1024: 45 us.
+// 131072 keys, 64 query heads on 8: 270 us (5.3 TB/s); 64 with a window of 1024: 44 us.
 //
 // A tile never goes through LDS. v_mfma_f32_16x16x32 with A = K (16 keys x 32 dimensions)
 // and B = q leaves lane l with scores of keys 4 (l / 16) + i of query row l % 16. The two

@@ -195,7 +195,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
   const int my_row = wave * kWaveRows + m32;
   const int pos = pos_of(my_row), tok = pos - first_pos;
   const int head = kv_head * a.group + head0 + min(my_row, rows - 1) - (tok - tok0) * a.group;
-  const int wave_p0 = pos_of(wave * kWaveRows), wave_p1 = pos_of(wave * kWaveRows + kWaveRows - 1);
+  const int wave_p1 = pos_of(wave * kWaveRows + kWaveRows - 1);
   const int wg_p0 = first_pos + tok0, wg_p1 = pos_of(kTileM - 1);
   const Keys keys = n > 0 ? keys_of(a, prefix, n, wg_p0, wg_p1, BN) : Keys{0, 0, 0};
   // this chunk's tiles of keys
