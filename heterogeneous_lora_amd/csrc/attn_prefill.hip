@@ -26,7 +26,7 @@
 // Two prompts of 8000 tokens after 7000-8192 cached, 32 query heads on 8 KV heads of 128,
 // bf16: 3.2 ms (970 TFLOP/s), with softcap 3.6 ms (860; it triples the transcendentals). A
 // library product of 8192^3 reaches 1262 on the same card. 64 prompts of 8 to 512 tokens, 32
-// heads of 128: 190 us.
+// heads of 128: 187 us.
 #include "attn_dev.h"
 
 namespace slora {
@@ -452,6 +452,8 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) frag[i] = k_frag(k_place, i);
     uint64_t row = row_of(t, 0);
+    // A wave with products to issue goes before one at a tile's border (long prompts -2%).
+    __builtin_amdgcn_s_setprio(1);
     __builtin_amdgcn_sched_barrier(0);
     uint4 vfrag[kSteps];
 #pragma unroll
@@ -488,6 +490,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
       }
       __builtin_amdgcn_sched_barrier(0);
     }
+    __builtin_amdgcn_s_setprio(0);
     // (the compiler would move the sum and the scores behind the branch)
     l = settled(l);
 #pragma unroll
