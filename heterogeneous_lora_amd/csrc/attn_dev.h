@@ -167,6 +167,22 @@ __device__ __forceinline__ uint32_t round2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf162_t));
 }
 
+// Two weights (>= 0) as a sum of two storage values each: one cut off towards zero and the
+// rounded rest, which leaves 2^-15 (bf16) or 2^-21 (f16, down to 2^-24 in all) of the weight.
+// Where the first is above zero so is the rest, as times an infinity in V a zero makes a NaN.
+template <int DT>
+__device__ __forceinline__ void split2(float x, float y, uint32_t* top, uint32_t* rest) {
+  if constexpr (DT == SLORA_F16) {
+    const float least = 0x1p-24f;  // of the type
+    *top = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(x, y));
+    *rest = round2<DT>(fmaxf(x - lo_f32<DT>(*top), fminf(x, least)), fmaxf(y - hi_f32<DT>(*top), fminf(y, least)));
+  } else {
+    const float below = 1.0f - 0x1p-10f;
+    *top = pair_hi(__float_as_uint(x * below), __float_as_uint(y * below));
+    *rest = round2<DT>(x - lo_f32<DT>(*top), y - hi_f32<DT>(*top));
+  }
+}
+
 // Partial results travel between workgroups, on other XCDs as well: stored and loaded at
 // the device's coherence point.
 __device__ __forceinline__ void put_pair(float* p, float x, float y) {
