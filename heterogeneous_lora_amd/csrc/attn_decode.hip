@@ -272,7 +272,7 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
     for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i]);
     mx = max32(max16(mx));
     // The maximum is moved only when it has grown by kRescale: until then the weights
-    // reach 2^kRescale, which costs neither range nor precision in 32 bits.
+    // reach 2^kRescale (times 2^kWeightLog2, which f16 holds).
     if (__any(mx > m + kRescale)) {
       const float mn = fmaxf(m, mx);
       const float f = part_weight(m, mn);
@@ -283,7 +283,7 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
 #pragma unroll
         for (int e = 0; e < VD; ++e) acc[h][e] *= f;
     }
-    const float ms = m == -INFINITY ? 0.f : m;
+    const float ms = (m == -INFINITY ? 0.f : m) - kWeightLog2<DT>;
     // The matrix unit takes weights of the storage type. Rounded to it once they would bring as
     // much error as the result's own rounding, so each goes in as two values and two products:
     // loads are what this kernel waits for (512 requests 1889 us, with one product each 1893).
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
         if constexpr (VD == 8) st16(o + d, make_uint4(w[0], w[1], w[2], w[3]));
         else *reinterpret_cast<uint2*>(o + d) = make_uint2(w[0], w[1]);
       }
-    if (a.lse && g == 0) a.lse[(int64_t)r * heads_q + head] = seen.bad ? NAN : m * kLn2 + logf(l);
+    if (a.lse && g == 0) a.lse[(int64_t)r * heads_q + head] = seen.bad ? NAN : log_sum<DT>(m, l);
     return;
   }
 
@@ -401,7 +401,7 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
       const float inv = lt == 0.f ? 0.f : 1.0f / lt;
       *reinterpret_cast<uint32_t*>(a.out + (int64_t)r * a.o_ts + (int64_t)hq * a.o_hs + d) =
           round2<DT>(seen.bad ? NAN : lt == 0.f ? 0.f : x * inv, seen.bad ? NAN : lt == 0.f ? 0.f : y * inv);
-      if (a.lse && d == 0) a.lse[(int64_t)r * heads_q + hq] = seen.bad ? NAN : mt * kLn2 + logf(lt);
+      if (a.lse && d == 0) a.lse[(int64_t)r * heads_q + hq] = seen.bad ? NAN : log_sum<DT>(mt, lt);
     } else {
       float* part = a.part + (int64_t)x_chunk * part_chunk + hq * part_row;
       put_pair(part + 2 + d, x, y);
@@ -463,7 +463,7 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
         *reinterpret_cast<uint32_t*>(a.out + (int64_t)r * a.o_ts + (int64_t)hq * a.o_hs + d) =
             lt == 0.f ? 0u : round2<DT>(o[e][0] / lt, o[e][1] / lt);
     }
-    if (a.lse && lane == 0) a.lse[(int64_t)r * heads_q + hq] = mt * kLn2 + logf(lt);
+    if (a.lse && lane == 0) a.lse[(int64_t)r * heads_q + hq] = log_sum<DT>(mt, lt);
   }
 }
 

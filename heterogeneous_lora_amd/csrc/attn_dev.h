@@ -167,6 +167,17 @@ __device__ __forceinline__ uint32_t round2(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf162_t));
 }
 
+// Weights are exp2(score - maximum + this). The maximum may lag by 8 (kRescale), so f16's
+// weights, which reach 2^15, keep all bits down to 2^-21 of the largest and some down to 2^-31
+// (at 0 it would be 2^-14 and 2^-24: 131072 keys of a long cache could vanish together).
+template <int DT>
+constexpr float kWeightLog2 = DT == SLORA_F16 ? 7.0f : 0.0f;
+// log(sum exp(s)) of a row from its maximum and its sum of weights.
+template <int DT>
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return (m - kWeightLog2<DT>) * kLn2 + logf(l);
+}
+
 // Two weights (>= 0) as a sum of two storage values each: one cut off towards zero and the
 // rounded rest, which leaves 2^-15 (bf16) or 2^-21 (f16, down to 2^-24 in all) of the weight.
 // Where the first is above zero so is the rest, as times an infinity in V a zero makes a NaN.

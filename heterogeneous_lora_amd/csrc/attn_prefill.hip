@@ -425,7 +425,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
       continue;
     }
     // The maximum is moved only when it has grown by kRescale: until then the weights
-    // reach 2^kRescale, which costs neither range nor precision in 32 bits.
+    // reach 2^kRescale (times 2^kWeightLog2, which f16 holds).
     if (__any(mx > m + kRescale)) {
       const float mn = fmaxf(m, mx);
       const float f = part_weight(m, mn);
@@ -440,7 +440,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
     // before its product, and waits for each): fragments are read kAhead products early.
     f32x16 sn[KT];
     uint32_t p[KT * 8];
-    const float ms = (MODE == kCap ? a.cap_out : 0.f) - (m == -INFINITY ? 0.f : m);
+    const float ms = (MODE == kCap ? a.cap_out : 0.f) + kWeightLog2<DT> - (m == -INFINITY ? 0.f : m);
     const bool edge_next = !all_seen(t + 1, wg_p0, wg_p1);
     const float far = far_of(t + 1);
     const uint32_t k_place = k_base + ((t + 1) & 1) * S::kUnits * 16, v_place = v_base + (t & 1) * S::kUnits * 16;
@@ -597,7 +597,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
       }
     }
   if (a.lse && h == 0)
-    a.lse[(int64_t)(q0 + tok) * (a.hk * a.group) + head] = bad ? NAN : m * kLn2 + logf(l);
+    a.lse[(int64_t)(q0 + tok) * (a.hk * a.group) + head] = bad ? NAN : log_sum<DT>(m, l);
 }
 
 template <int DT, int MODE>

@@ -580,8 +580,9 @@ int slora_kv_write(const slora_kv* kv, const slora_qkv* qkv, void* stream);
  * + slopes[h] * (j - p) if slopes is given; out = sum_j softmax(s)_j v_j and lse =
  * log(sum_j exp(s_j)). Scores, statistics and sums are in 32 bits. For the product with V
  * the weights exp(s - max) are in slora_attn_decode sums of two values of the storage type
- * (2^-15 of a weight is lost in bf16; 2^-21 in f16, and 2^-24 of the largest), in
- * slora_attn_prefill rounded to it once. Keys no query of a row
+ * (2^-15 of a weight is lost in bf16; 2^-21 in f16, and 2^-31 of the largest), in
+ * slora_attn_prefill rounded to it once (2^-8 and 2^-11 of a weight; in f16 2^-32 of the
+ * largest if that is more). Keys no query of a row
  * sees (a request's other rows', unwritten places, the tail of a page) do not touch that
  * row, whatever they hold. A row that sees no key, or only scores of minus infinity, is
  * 0 with lse minus infinity. A page id outside the pool reads as NaN, as in the LoRA calls, and a seq_len
