@@ -347,7 +347,9 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
       for (int i = 0; i < 16; ++i) x = MODE == kCap ? fminf(x, s[kt][i]) : fmaxf(x, s[kt][i]);
     return MODE == kCap ? __builtin_fmaf(-max32(-x), mul, a.cap_out) : max32(x) * mul;
   };
-  // Weights 2 j and 2 j + 1, their part of the sum and of the B operand.
+  // Weights 2 j and 2 j + 1, their part of the sum and of the B operand. They are rounded to the
+  // storage type once, the usual trade: as sums of two values, with two products each, long
+  // prompts take 4683 us against 3666 and 64 short ones 215 against 188.
   auto weight_pair = [&](const f32x16 (&s)[KT], float ms, uint32_t (&p)[KT * 8], int j) {
     const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j / 8][j % 8 * 2], mul, ms));
     const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j / 8][j % 8 * 2 + 1], mul, ms));
