@@ -335,7 +335,9 @@ class KVCache:
 
     Each bind_* method checks shapes and types, marshals one call's arguments once and
     returns a no-argument callable; the method of the same name without bind_ makes the call
-    at once. Calls go to `stream` (the current stream at binding if None)."""
+    at once. Calls go to `stream` (the current stream at binding if None), which the caller
+    orders with the work that makes and uses their tensors. A workspace that is not given is
+    made, zeroed and, with the bound call, freed on that stream."""
 
     def __init__(self, pool: Optional[torch.Tensor], n_pages: int, page_elems: int = 0, dtype: str = "f16",
                  n_kv_heads: int = 1, head_dim: int = 8, tokens_per_page: int = 1):
@@ -438,9 +440,12 @@ class KVCache:
         a.slopes, a.prefix_len, a.lse = _opt(slopes), _opt(prefix_len), _opt(lse)
         return a, self._kv(n_req, max_blocks), (self.pool, q, out, k_table, v_table, seq_len, slopes, prefix_len, lse)
 
-    def _ws(self, kv, a, n_tokens, ws, device):
+    def _ws(self, kv, a, n_tokens, ws, device, stream):
         need = _lib.attn_workspace_size(kv, a, n_tokens)
-        return torch.zeros(need, dtype=torch.uint8, device=device) if ws is None else ws
+        if ws is not None:
+            return ws
+        with torch.cuda.stream(stream):  # (None: the current one)
+            return torch.zeros(need, dtype=torch.uint8, device=device)
 
     def bind_decode(self, q: torch.Tensor, out: torch.Tensor, k_table: torch.Tensor, v_table: torch.Tensor,
                     seq_len: torch.Tensor, scale: Optional[float] = None, softcap: float = 0.0,
@@ -451,16 +456,13 @@ class KVCache:
             raise ValueError(f"q: {q.shape[0]} rows for {k_table.shape[0]} requests")
         a, kv, tensors = self._attn(q, out, k_table, v_table, seq_len, scale, softcap, window, slopes,
                                     prefix_len, lse)
-        ws = self._ws(kv, a, 0, ws, q.device)
+        ws = self._ws(kv, a, 0, ws, q.device, stream)
         call = _lib.bind_attn_decode(kv, a, ws.data_ptr(), ws.numel(), self._stream(q, stream))
         call.tensors = tensors + (ws,)
         return call
 
-    def decode(self, *args, stream: Optional[torch.cuda.Stream] = None, **kw):
-        call = self.bind_decode(*args, stream=stream, **kw)
-        call()
-        if stream is not None:  # a workspace made here goes back to its own stream's memory
-            call.tensors[-1].record_stream(stream)
+    def decode(self, *args, **kw):
+        self.bind_decode(*args, **kw)()
 
     def bind_prefill(self, q: torch.Tensor, out: torch.Tensor, k_table: torch.Tensor, v_table: torch.Tensor,
                      seq_len: torch.Tensor, q_offsets: torch.Tensor, scale: Optional[float] = None,
@@ -470,17 +472,14 @@ class KVCache:
         _expect("q_offsets", q_offsets, torch.int32, (k_table.shape[0] + 1,))
         a, kv, tensors = self._attn(q, out, k_table, v_table, seq_len, scale, softcap, window, slopes,
                                     prefix_len, lse)
-        ws = self._ws(kv, a, q.shape[0], ws, q.device)
+        ws = self._ws(kv, a, q.shape[0], ws, q.device, stream)
         call = _lib.bind_attn_prefill(kv, a, q_offsets.data_ptr(), q.shape[0], ws.data_ptr(), ws.numel(),
                                       self._stream(q, stream))
         call.tensors = tensors + (q_offsets, ws)
         return call
 
-    def prefill(self, *args, stream: Optional[torch.cuda.Stream] = None, **kw):
-        call = self.bind_prefill(*args, stream=stream, **kw)
-        call()
-        if stream is not None:  # a workspace made here goes back to its own stream's memory
-            call.tensors[-1].record_stream(stream)
+    def prefill(self, *args, **kw):
+        self.bind_prefill(*args, **kw)()
 
 
 class AttentionLoop(ServingLoop):
