@@ -200,6 +200,9 @@ class ServingLoop:
     step's batch (new prompts as segments, one decode token per running request) runs
     through slora_apply on the compute stream once the fetch event has fired.
 
+    Everything a step does runs on the stream that is current when the loop is made (or on
+    the side stream, ordered with it), whatever stream is current in step().
+
     Every adapter the workload defines is in the host store; only the pool's pages limit
     how many are resident at once. The weights, x and y0 of a step are seeded synthetic
     data (the same generators the tests and the oracle use)."""
@@ -234,11 +237,12 @@ class ServingLoop:
     def step(self, seed: int):
         """Plan one step, fetch what it needs, run its batch. Returns (batch dict, x, y0, y)
         as host arrays (uint16 bits) for checking, or the batch alone when it is empty."""
-        b, x, y0, yd = self._project(seed)
-        return b, x, y0, None if yd is None else yd.cpu().numpy().view(np.uint16)
+        with torch.cuda.stream(self.stream):
+            b, x, y0, yd = self._project(seed)
+            return b, x, y0, None if yd is None else yd.cpu().numpy().view(np.uint16)
 
     def _project(self, seed: int):
-        """step(), with y left on the device."""
+        """step(), with y left on the device. self.stream is the current stream."""
         b = self.sched.step()
         if b["fetch"].size:
             done = torch.cuda.Event()
@@ -516,7 +520,18 @@ class AttentionLoop(ServingLoop):
     def step(self, seed: int):
         """One step. Returns (batch dict, qkv, out) with the projections [tokens, heads, head_dim]
         (queries, keys, values) and the attention's output [tokens, n_q_heads, head_dim] on the
-        device, in the batch's order: new prompts' tokens, then one of each running request."""
+        device, in the batch's order: new prompts' tokens, then one of each running request. The
+        current stream waits for them."""
+        with torch.cuda.stream(self.stream):
+            b, qkv, out = self._step(seed)
+        user = torch.cuda.current_stream(self.device)
+        if out is not None and user != self.stream:
+            user.wait_stream(self.stream)
+            for t in (qkv, out):
+                t.record_stream(user)
+        return b, qkv, out
+
+    def _step(self, seed: int):
         b, _, _, y = self._project(seed)
         gone = [int(r) for r in np.concatenate([b["finished"], b["aborted"]])]
         for r in gone:
