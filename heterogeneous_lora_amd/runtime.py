@@ -324,10 +324,17 @@ class KVTables:
         self.slots = ints(n_planes, n_tokens, dtype=torch.int64)
 
 
-def _expect(name: str, t: torch.Tensor, dtype, shape):
+def _on_gpu(name: str, t: torch.Tensor, device: Optional[torch.device] = None):
+    """Kernels follow a tensor's address: one in host memory, or another GPU's, is refused."""
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name}: expected a tensor on {'the GPU' if device is None else device}, got one on {t.device}")
+
+
+def _expect(name: str, t: torch.Tensor, dtype, shape, device: Optional[torch.device] = None):
     if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got "
                          f"{t.dtype} {tuple(t.shape)}")
+    _on_gpu(name, t, device)
 
 
 def _opt(t: Optional[torch.Tensor]):
@@ -347,8 +354,13 @@ class KVCache:
                  n_kv_heads: int = 1, head_dim: int = 8, tokens_per_page: int = 1):
         if pool is not None and pool.numel() * pool.element_size() < 2 * n_pages * page_elems:
             raise ValueError(f"pool holds fewer than {n_pages} pages of {page_elems} elements")
+        if pool is not None:
+            _on_gpu("pool", pool)
+            if not pool.is_contiguous():
+                raise ValueError("pool: expected a contiguous tensor")
         self.pool, self.n_pages, self.page_elems, self.dtype = pool, n_pages, page_elems, dtype
         self.n_kv_heads, self.head_dim, self.tokens_per_page = n_kv_heads, head_dim, tokens_per_page
+        self.device = None if pool is None else pool.device
 
     def _kv(self, n_requests: int = 0, max_blocks: int = 0) -> _lib.KV:
         return _lib.KV(_opt(self.pool), self.n_pages, self.page_elems, _lib.DTYPES[self.dtype],
@@ -362,6 +374,7 @@ class KVCache:
             want = f"[{'rows' if n is None else n}, {'heads' if heads is None else heads}, {self.head_dim}]"
             raise ValueError(f"{name}: expected {TORCH_DTYPES[self.dtype]} {want} with a dense last dimension, "
                              f"got {t.dtype} {tuple(t.shape)}")
+        _on_gpu(name, t, self.device)
         return t.data_ptr(), t.stride(0), t.stride(1)
 
     @staticmethod
@@ -373,9 +386,9 @@ class KVCache:
                     new_len: torch.Tensor, append: bool = False,
                     stream: Optional[torch.cuda.Stream] = None):
         t = tables
-        _expect("pages", pages, torch.int32, (pages.numel(),))
-        _expect("past_len", past_len, torch.int32, (t.n_requests,))
-        _expect("new_len", new_len, torch.int32, (t.n_requests,))
+        _expect("pages", pages, torch.int32, (pages.numel(),), t.table.device)
+        _expect("past_len", past_len, torch.int32, (t.n_requests,), t.table.device)
+        _expect("new_len", new_len, torch.int32, (t.n_requests,), t.table.device)
         step = _lib.KVStep(t.n_planes, int(append), pages.data_ptr(), pages.numel(), past_len.data_ptr(),
                            new_len.data_ptr(), t.n_tokens, t.table.data_ptr(), t.seq_len.data_ptr(),
                            t.q_offsets.data_ptr(), t.token_request.data_ptr(), t.position.data_ptr(),
@@ -402,18 +415,19 @@ class KVCache:
             w.k, w.k_token_stride, w.k_head_stride = self._rows("k", k, n, self.n_kv_heads)
             w.v, w.v_token_stride, w.v_head_stride = self._rows("v", v, n, self.n_kv_heads)
             for name, s in (("k_slots", k_slots), ("v_slots", v_slots)):
-                _expect(name, s, torch.int64, (n,))
+                _expect(name, s, torch.int64, (n,), q.device)
             w.k_slots, w.v_slots = k_slots.data_ptr(), v_slots.data_ptr()
         elif k is not None or v is not None:
             raise ValueError("k and v are given together or not at all")
-        _expect("position", position, torch.int32, (n,))
+        _expect("position", position, torch.int32, (n,), q.device)
         w.position = position.data_ptr()
         if rope is not None:
+            _expect("rope.turns", rope.turns, torch.float64, (rope.rotary_dim // 2,), q.device)
             w.turns, w.rotary_dim, w.interleaved = rope.turns.data_ptr(), rope.rotary_dim, int(rope.interleaved)
             w.cos_sin_scale = rope.cos_sin_scale
         for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
             if t is not None:
-                _expect(name, t, TORCH_DTYPES[self.dtype], (self.head_dim,))
+                _expect(name, t, TORCH_DTYPES[self.dtype], (self.head_dim,), q.device)
         w.norm, w.eps, w.q_weight, w.k_weight = int(norm), eps, _opt(q_weight), _opt(k_weight)
         call = _lib.bind_kv_write(self._kv(), w, self._stream(q, stream))
         call.tensors = (self.pool, q, k, v, q_out, position, k_slots, v_slots, rope, q_weight, k_weight)
@@ -431,15 +445,15 @@ class KVCache:
         a.softcap, a.window = softcap, window
         a.q, a.q_token_stride, a.q_head_stride = self._rows("q", q)
         a.out, a.out_token_stride, a.out_head_stride = self._rows("out", out, q.shape[0], q.shape[1])
-        _expect("k_table", k_table, torch.int32, (n_req, max_blocks))
-        _expect("v_table", v_table, torch.int32, (n_req, max_blocks))
-        _expect("seq_len", seq_len, torch.int32, (n_req,))
+        _expect("k_table", k_table, torch.int32, (n_req, max_blocks), q.device)
+        _expect("v_table", v_table, torch.int32, (n_req, max_blocks), q.device)
+        _expect("seq_len", seq_len, torch.int32, (n_req,), q.device)
         if slopes is not None:
-            _expect("slopes", slopes, torch.float32, (q.shape[1],))
+            _expect("slopes", slopes, torch.float32, (q.shape[1],), q.device)
         if prefix_len is not None:
-            _expect("prefix_len", prefix_len, torch.int32, (n_req,))
+            _expect("prefix_len", prefix_len, torch.int32, (n_req,), q.device)
         if lse is not None:
-            _expect("lse", lse, torch.float32, (q.shape[0], q.shape[1]))
+            _expect("lse", lse, torch.float32, (q.shape[0], q.shape[1]), q.device)
         a.k_table, a.v_table, a.seq_len = k_table.data_ptr(), v_table.data_ptr(), seq_len.data_ptr()
         a.slopes, a.prefix_len, a.lse = _opt(slopes), _opt(prefix_len), _opt(lse)
         return a, self._kv(n_req, max_blocks), (self.pool, q, out, k_table, v_table, seq_len, slopes, prefix_len, lse)
@@ -447,6 +461,9 @@ class KVCache:
     def _ws(self, kv, a, n_tokens, ws, device, stream):
         need = _lib.attn_workspace_size(kv, a, n_tokens)
         if ws is not None:
+            _on_gpu("ws", ws, device)
+            if not ws.is_contiguous():
+                raise ValueError("ws: expected a contiguous tensor")
             return ws
         with torch.cuda.stream(stream):  # (None: the current one)
             return torch.zeros(need, dtype=torch.uint8, device=device)
@@ -461,7 +478,7 @@ class KVCache:
         a, kv, tensors = self._attn(q, out, k_table, v_table, seq_len, scale, softcap, window, slopes,
                                     prefix_len, lse)
         ws = self._ws(kv, a, 0, ws, q.device, stream)
-        call = _lib.bind_attn_decode(kv, a, ws.data_ptr(), ws.numel(), self._stream(q, stream))
+        call = _lib.bind_attn_decode(kv, a, ws.data_ptr(), ws.nbytes, self._stream(q, stream))
         call.tensors = tensors + (ws,)
         return call
 
@@ -473,11 +490,11 @@ class KVCache:
                      softcap: float = 0.0, window: int = 0, slopes: Optional[torch.Tensor] = None,
                      prefix_len: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                      ws: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
-        _expect("q_offsets", q_offsets, torch.int32, (k_table.shape[0] + 1,))
         a, kv, tensors = self._attn(q, out, k_table, v_table, seq_len, scale, softcap, window, slopes,
                                     prefix_len, lse)
+        _expect("q_offsets", q_offsets, torch.int32, (k_table.shape[0] + 1,), q.device)
         ws = self._ws(kv, a, q.shape[0], ws, q.device, stream)
-        call = _lib.bind_attn_prefill(kv, a, q_offsets.data_ptr(), q.shape[0], ws.data_ptr(), ws.numel(),
+        call = _lib.bind_attn_prefill(kv, a, q_offsets.data_ptr(), q.shape[0], ws.data_ptr(), ws.nbytes,
                                       self._stream(q, stream))
         call.tensors = tensors + (q_offsets, ws)
         return call
