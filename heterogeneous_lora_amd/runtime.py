@@ -510,7 +510,7 @@ class AttentionLoop(ServingLoop):
     running requests' new tokens over their caches (slora_attn_decode).
 
     d_out of the projection is (n_q_heads + 2 n_kv_heads) * head_dim; max_len bounds a
-    request's tokens. attention: softcap, window, slopes, scale as KVCache.bind_decode takes
+    request's cached tokens. attention: softcap, window, slopes, scale as KVCache.bind_decode takes
     them; write: norm, q_weight, k_weight, eps as KVCache.bind_write does."""
 
     def __init__(self, wl, n_pages: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_len: int,
@@ -533,6 +533,14 @@ class AttentionLoop(ServingLoop):
         if self.ws is None or self.ws.numel() < need:
             self.ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
         return self.ws
+
+    def submit(self, request_id, adapter_id, prompt_len, max_new_tokens, deadline_step=-1):
+        """As ServingLoop.submit. A request's prompt and all but the last of its new tokens are
+        cached, at most max_len of them."""
+        if prompt_len + max_new_tokens - 1 > self.max_len:
+            raise ValueError(f"request {request_id}: a prompt of {prompt_len} and {max_new_tokens} new tokens pass "
+                             f"{self.max_len} cached tokens")
+        super().submit(request_id, adapter_id, prompt_len, max_new_tokens, deadline_step)
 
     def step(self, seed: int):
         """One step. Returns (batch dict, qkv, out) with the projections [tokens, heads, head_dim]
@@ -559,8 +567,6 @@ class AttentionLoop(ServingLoop):
         new = np.concatenate([np.diff(b["seg_offsets"]), np.ones(len(running), np.int32)]).astype(np.int32)
         requests = prompts + running
         past = np.array([self.cached.get(r, 0) for r in requests], np.int32)
-        if int((past + new).max()) > self.max_len:
-            raise ValueError(f"a request passes {self.max_len} tokens")
         dev = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(self.device)
         pages = np.concatenate([self.sched.request_pages(r) for r in requests])
         T, S, first = b["n_tokens"], len(prompts), int(b["seg_offsets"][-1])
