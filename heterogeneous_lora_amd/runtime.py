@@ -558,15 +558,14 @@ class AttentionLoop(ServingLoop):
 
     def _step(self, seed: int):
         b, _, _, y = self._project(seed)
-        gone = [int(r) for r in np.concatenate([b["finished"], b["aborted"]])]
-        for r in gone:
-            self.cached.pop(r, None)
         if y is None:
+            self.cached = {}
             return b, None, None
         prompts, running = [int(r) for r in b["seg_request"]], [int(r) for r in b["token_request"]]
         new = np.concatenate([np.diff(b["seg_offsets"]), np.ones(len(running), np.int32)]).astype(np.int32)
         requests = prompts + running
-        past = np.array([self.cached.get(r, 0) for r in requests], np.int32)
+        # a new prompt has nothing cached, also where its id has run before
+        past = np.array([0] * len(prompts) + [self.cached[r] for r in running], np.int32)
         dev = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(self.device)
         pages = np.concatenate([self.sched.request_pages(r) for r in requests])
         T, S, first = b["n_tokens"], len(prompts), int(b["seg_offsets"][-1])
@@ -584,6 +583,5 @@ class AttentionLoop(ServingLoop):
         if running:
             self.cache.decode(rotated[first:], out[first:], t.table[0, S:], t.table[1, S:], t.seq_len[S:],
                               ws=ws, **self.attention)
-        for r, n in zip(requests, past + new):
-            self.cached[r] = int(n)
+        self.cached = {r: int(n) for r, n in zip(requests, past + new)}  # (a step has every running request)
         return b, qkv, out
