@@ -252,9 +252,12 @@ __global__ __launch_bounds__(kWaves * 64, NC <= 4 ? 2 : 1) void attn_decode_kern
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[u * 4 + i] = c4[i];
     }
-    if (a.cap_out != 0.f) {
+    if (a.cap_out > kNearCap * kLog2e) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] = capped(a, s[i]);
+    } else if (a.cap_out != 0.f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = capped_near(a, s[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] *= a.scale2;

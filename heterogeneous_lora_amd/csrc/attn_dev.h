@@ -85,11 +85,23 @@ __device__ __forceinline__ uint64_t key_addr(const AttnArgs& a, int32_t page, in
   return (uint32_t)page < a.n_pages_u ? at : nans;
 }
 
-// Score in units of log 2 (weights are exp2 of differences).
-__device__ __forceinline__ float capped(const AttnArgs& a, float s) {
-  // cap tanh(x / cap) = cap - 2 cap / (exp(2 x / cap) + 1)
+// Softcap of a product, in units of log 2 (weights are exp2 of differences), as
+//   cap tanh(x / cap) = cap - 2 cap / (exp(2 x / cap) + 1),
+// whose error is 2^-22 cap whatever the score: for caps up to kNearCap, where that is 2^-14
+// beside 2^-11 (f16) and 2^-8 of a weight's rounding to the storage type.
+constexpr float kNearCap = 256.0f;
+__device__ __forceinline__ float capped_near(const AttnArgs& a, float s) {
   const float e = __builtin_amdgcn_exp2f(s * a.cap_in);
   return a.cap_out - 2.0f * a.cap_out * __builtin_amdgcn_rcpf(e + 1.0f);
+}
+// For any cap: where |y| = |x / cap| < 1/8 the odd series of tanh, x (1 - y^2 / 3 + 2 y^4 / 15)
+// (the next term is below 2^-22), else the form above; off by 2^-19 of the score at most. (z
+// is the square of 2 log2(e) y.)
+__device__ __forceinline__ float capped(const AttnArgs& a, float s) {
+  constexpr float k = kLn2 * kLn2 / 4;
+  const float y = s * a.cap_in, z = y * y;
+  const float p = __builtin_fmaf(z, __builtin_fmaf(z, 2.0f / 15 * k * k, -1.0f / 3 * k), 1.0f);
+  return z < 0x1p-6f / k ? s * a.scale2 * p : capped_near(a, s);
 }
 
 template <int DT>

@@ -160,7 +160,9 @@ __device__ __forceinline__ uint2 read_turned(uint32_t at, int off) {
 // What a score passes through between the two products. kPlain: the scale alone, taken in
 // the subtraction of the maximum. kCap: softcap. kBias, kBiasCap: a bias that depends on
 // distance after them, and scales of zero or below (which would turn a masked -infinity).
-enum Mode { kPlain, kCap, kBias, kBiasCap };
+// kWideCap: a softcap above kNearCap, with or without them, in the form that holds there (long
+// prompts without a bias 5022 us, kCap 3748: two forms a score, and 19 registers that spill).
+enum Mode { kPlain, kCap, kBias, kBiasCap, kWideCap };
 
 // Two workgroups a CU leave a wave 256 registers: heads up to 192 fit (192: 2.4 ms against 3.8
 // with one workgroup), 256 would spill (9.4 ms against 4.6).
@@ -319,7 +321,8 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
       const int i = j % 8 * 2 + e;
       float x = s[kt][i];
       if (MODE == kCap) x = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * a.cap_in) + 1.0f);
-      else if (MODE == kBiasCap) x = capped(a, x);
+      else if (MODE == kBiasCap) x = capped_near(a, x);
+      else if (MODE == kWideCap) x = capped(a, x);
       else if (MODE == kBias) x *= a.scale2;
       if (MODE >= kBias) x = __builtin_fmaf(slope, far + (float)(kt * 32 + 16 * (i / 8) + i % 8), x);
       s[kt][i] = x;
@@ -622,6 +625,7 @@ hipError_t launch_mode(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev)
 template <int DT>
 hipError_t launch_dt(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev) {
   const bool cap = a.cap_out != 0.f, bias = a.slopes || !(a.scale2 > 0.f);
+  if (a.cap_out > kNearCap * kLog2e) return launch_mode<DT, kWideCap>(a, s, ev);
   return bias && cap ? launch_mode<DT, kBiasCap>(a, s, ev)
          : bias      ? launch_mode<DT, kBias>(a, s, ev)
          : cap       ? launch_mode<DT, kCap>(a, s, ev)

@@ -1,6 +1,9 @@
 // KV cache and attention entry points: argument checks and kernel arguments. Everything
 // that depends on device data (lengths, tables, slots) is checked by the kernels.
+#include <float.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "guard.h"
 #include "internal.h"
@@ -218,7 +221,8 @@ int attn_args(const char* what, const slora_kv* kv, const slora_attn* at, void* 
   const double log2e = 1.4426950408889634;
   a->scale2 = (float)(at->scale * log2e);
   if (at->softcap > 0.f) {
-    a->cap_in = (float)(2.0 * log2e * at->scale / at->softcap);
+    // (finite: times a score of 0 it is 0; cap_out may be infinite, its form is then not used)
+    a->cap_in = (float)std::clamp(2.0 * log2e * at->scale / at->softcap, -(double)FLT_MAX, (double)FLT_MAX);
     a->cap_out = (float)(at->softcap * log2e);
   }
   a->window = at->window;

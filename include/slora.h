@@ -578,7 +578,8 @@ int slora_kv_write(const slora_kv* kv, const slora_qkv* qkv, void* stream);
  *   (j <= p and (window == 0 or j > p - window)) or (prefix_len and j < prefix_len[r]);
  * its score is s = scale * q.k_j, then softcap * tanh(s / softcap) if softcap > 0, then
  * + slopes[h] * (j - p) if slopes is given; out = sum_j softmax(s)_j v_j and lse =
- * log(sum_j exp(s_j)). Scores, statistics and sums are in 32 bits. For the product with V
+ * log(sum_j exp(s_j)). Scores, statistics and sums are in 32 bits (a softcap up to
+ * 256 brings an error of 2^-22 of the cap, a larger one of 2^-19 of the score). For the product with V
  * the weights exp(s - max) are in slora_attn_decode sums of two values of the storage type
  * (2^-15 of a weight is lost in bf16; 2^-21 in f16, and 2^-31 of the largest), in
  * slora_attn_prefill rounded to it once (2^-8 and 2^-11 of a weight; in f16 2^-32 of the

@@ -5,8 +5,8 @@ A row's result is off by at most
   (weight + 2 d + 2^-18) sum_j w_j |v_j|  +  floor sum_j |v_j|  +  u |out|
 weight: the part of a weight that is lost on its way to the product with V; floor: what is
 lost whatever the weight, relative to the largest one; d: the error of a score, 2^-24 (D + 16)
-max_j scale * sum |q||k_j| for the products and 2^-22 max_j |s_j| for the roundings behind
-them; 2^-18: sums over keys in 32 bits; u: half a step of the storage type."""
+max_j scale * sum |q||k_j| for the products, 2^-22 max_j |s_j| for the roundings behind them
+and, with a softcap, 2^-22 cap up to 256, 2^-19 max_j |s_j| above; 2^-18: sums over keys in 32 bits; u: half a step of the storage type."""
 
 import math
 from types import SimpleNamespace
@@ -17,7 +17,7 @@ import torch
 from kv_util import TORCH, half_step
 
 
-def attention(c, q, rows, *, scale, cap=0.0, window=0, rounded=None):
+def attention(c, q, rows, *, scale, cap=0.0, window=0, slopes=None, rounded=None):
     """For `rows`, (request, position) of each row of q: out, mass = sum w |v|, total = sum |v|,
     d and lse. rounded: a type that the weights (relative to the largest) are rounded to, as a
     planted mistake."""
@@ -37,6 +37,9 @@ def attention(c, q, rows, *, scale, cap=0.0, window=0, rounded=None):
             d[i, h] = 2.0 ** -24 * (dim + 16) * float((k.abs() @ x.abs()).max()) * abs(scale)
             if cap:
                 s = cap * torch.tanh(s / cap)
+                d[i, h] += 2.0 ** -22 * cap if cap <= 256 else 2.0 ** -19 * float(s.abs().max())
+            if slopes is not None:
+                s = s + float(slopes[h]) * (j[seen].double() - p)
             d[i, h] += 2.0 ** -22 * float(s.abs().max())
             w = torch.exp(s - s.max())
             lse[i, h] = s.max() + torch.log(w.sum())
