@@ -225,7 +225,8 @@ int attn_args(const char* what, const slora_kv* kv, const slora_attn* at, void* 
     a->cap_in = (float)std::clamp(2.0 * log2e * at->scale / at->softcap, -(double)FLT_MAX, (double)FLT_MAX);
     a->cap_out = (float)(at->softcap * log2e);
   }
-  a->window = at->window;
+  // (a window that covers any request is none: positions minus it stay in range)
+  a->window = at->window < a->max_len ? at->window : 0;
   a->slopes = at->slopes;
   a->counters = (int32_t*)ws;
   a->part = (float*)((uint8_t*)ws + kAttnCounterBytes);
