@@ -675,9 +675,9 @@ hipError_t timed_fetch(const FetchPage* pages, int64_t n, uint16_t* pool, int32_
   });
 }
 
-hipError_t timed_call(int kernel, hipStream_t s, const std::function<hipError_t(const LaunchEvents&)>& launch) {
+hipError_t timed_call(int kernel, hipStream_t s, hipError_t (*launch)(const void*, const LaunchEvents&), const void* arg) {
   std::lock_guard<std::mutex> lk(g_mu);
-  return timed_launch(kernel, s, launch);
+  return timed_launch(kernel, s, [&](const LaunchEvents& ev) { return launch(arg, ev); });
 }
 
 int apply_shared(const slora_lora* L, const slora_routing* R, const void* x, void* y, void* ws,

@@ -4,7 +4,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <functional>
 #include <string>
 #include <vector>
 
@@ -334,6 +333,11 @@ hipError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, hipStream_t s, 
 hipError_t launch_kv_tables(const slora_kv& kv, const slora_kv_step& st, hipStream_t s, const LaunchEvents& ev);
 hipError_t launch_kv_write(const slora_kv& kv, const slora_qkv& w, hipStream_t s, const LaunchEvents& ev);
 // One call's launches, timed as kernel id `kernel` while kernel timing is on (api.cpp).
-hipError_t timed_call(int kernel, hipStream_t s, const std::function<hipError_t(const LaunchEvents&)>& launch);
+// `launch` is called before these return, so it is passed by address: a call allocates nothing.
+hipError_t timed_call(int kernel, hipStream_t s, hipError_t (*launch)(const void*, const LaunchEvents&), const void* arg);
+template <typename F>
+hipError_t timed_call(int kernel, hipStream_t s, const F& launch) {
+  return timed_call(kernel, s, [](const void* f, const LaunchEvents& ev) { return (*static_cast<const F*>(f))(ev); }, &launch);
+}
 
 }  // namespace slora

@@ -17,6 +17,14 @@
 #include "internal.h"
 
 static int64_t g_fail = 0, g_calls = 0, g_cut = 0, g_most_counters = 0, g_refused = 0;
+static int64_t g_allocations = 0;
+void* operator new(size_t n) {
+  ++g_allocations;
+  if (void* p = std::malloc(n ? n : 1)) return p;
+  throw std::bad_alloc();
+}
+void operator delete(void* p) noexcept { std::free(p); }
+void operator delete(void* p, size_t) noexcept { std::free(p); }
 #define CHECK(c)                                                                            \
   do {                                                                                      \
     if (!(c) && ++g_fail <= 20) std::fprintf(stderr, "check failed at line %d: %s\n", __LINE__, #c); \
@@ -45,8 +53,8 @@ int fail(int code, const char* fmt, ...) {
 int hip_fail(hipError_t, const char*) { return SLORA_E_HIP; }
 void clear_error() {}
 
-hipError_t timed_call(int, hipStream_t, const std::function<hipError_t(const LaunchEvents&)>& launch) {
-  return launch(LaunchEvents());
+hipError_t timed_call(int, hipStream_t, hipError_t (*launch)(const void*, const LaunchEvents&), const void* arg) {
+  return launch(arg, LaunchEvents());
 }
 
 // Keys that a request's last row sees.
@@ -287,8 +295,34 @@ static void any_round() {
   ok(slora_kv_write(&kv, &w, nullptr));
 }
 
+// The calls allocate nothing on the way to their launches.
+static void no_allocations() {
+  slora_kv kv = make_kv(2, 64, 2, 3, 8);
+  slora_attn at = make_attn(4, 64);
+  slora_kv_step st;
+  memset(&st, 0, sizeof st);
+  st.n_planes = 2;
+  st.past_len = st.new_len = (const int32_t*)kFakeDev;
+  st.tables = st.seq_len = st.q_offsets = (int32_t*)kFakeDev;
+  slora_qkv w;
+  memset(&w, 0, sizeof w);
+  w.n_tokens = w.n_q_heads = 4;
+  w.q = w.q_out = kFakeDev;
+  w.position = (const int32_t*)kFakeDev;
+  g_seq.assign(3, 8);
+  g_new.assign(3, 1);
+  const int64_t calls = g_calls, before = g_allocations;
+  g_ws_bytes = 1 << 20;
+  CHECK(slora_kv_tables(&kv, &st, nullptr) == SLORA_OK);
+  CHECK(slora_kv_write(&kv, &w, nullptr) == SLORA_OK);
+  CHECK(slora_attn_decode(&kv, &at, kFakeDev, g_ws_bytes, nullptr) == SLORA_OK);
+  CHECK(slora_attn_prefill(&kv, &at, (const int32_t*)kFakeDev, 3, kFakeDev, g_ws_bytes, nullptr) == SLORA_OK);
+  CHECK(g_calls == calls + 4 && g_allocations == before);
+}
+
 int main(int argc, char** argv) {
   const int rounds = argc > 1 ? std::atoi(argv[1]) : 20;
+  no_allocations();
   divisors();
   counters_of_all_heads();
   for (int32_t hk : {1, 2, 3, 5, 8, 512, 513, 1021, 1024})  // few rows over long caches
@@ -297,7 +331,7 @@ int main(int argc, char** argv) {
         for (int32_t n_req : {1, 3, 40})
           attention(hk, group, 64, n_req, 1 << 20, 2 * n_req);
   for (int i = 0; i < rounds; ++i) {
-    attention_round();
+    for (int j = 0; j < 10; ++j) attention_round();
     for (int j = 0; j < 20; ++j) rope_round();
     for (int j = 0; j < 50; ++j) any_round();
   }
