@@ -578,16 +578,17 @@ int slora_kv_write(const slora_kv* kv, const slora_qkv* qkv, void* stream);
  *   (j <= p and (window == 0 or j > p - window)) or (prefix_len and j < prefix_len[r]);
  * its score is s = scale * q.k_j, then softcap * tanh(s / softcap) if softcap > 0, then
  * + slopes[h] * (j - p) if slopes is given; out = sum_j softmax(s)_j v_j and lse =
- * log(sum_j exp(s_j)). Scores, statistics and sums are in 32 bits (a softcap up to
- * 256 brings an error of 2^-22 of the cap, a larger one of 2^-19 of the score). For the product with V
- * the weights exp(s - max) are in slora_attn_decode sums of two values of the storage type
- * (2^-15 of a weight is lost in bf16; 2^-21 in f16, and 2^-31 of the largest), in
- * slora_attn_prefill rounded to it once (2^-8 and 2^-11 of a weight; in f16 2^-32 of the
- * largest if that is more). Keys no query of a row
- * sees (a request's other rows', unwritten places, the tail of a page) do not touch that
- * row, whatever they hold. A row that sees no key, or only scores of minus infinity, is
- * 0 with lse minus infinity. A page id outside the pool reads as NaN, as in the LoRA calls, and a seq_len
- * outside [0, max_blocks * tokens_per_page] makes the request's rows NaN.
+ * log(sum_j exp(s_j)). Scores, statistics and sums are in 32 bits (a softcap up to 256
+ * brings an error of 2^-22 of the cap, a larger one of 2^-19 of the score). For the
+ * product with V the weights exp(s - max) are in slora_attn_decode sums of two values of
+ * the storage type (2^-15 of a weight is lost in bf16; 2^-21 in f16, and 2^-31 of the
+ * largest), in slora_attn_prefill rounded to it once (2^-8 and 2^-11 of a weight; in f16
+ * 2^-32 of the largest if that is more). Keys no query of a row sees (a request's other
+ * rows', unwritten places, the tail of a page) do not touch that row, whatever they hold.
+ * A row that sees no key, or only scores of minus infinity, is 0 with lse minus infinity;
+ * positions below 0 (more new tokens than seq_len) see the prefix alone. A page id outside
+ * the pool reads as NaN, as in the LoRA calls, and a seq_len outside [0, max_blocks *
+ * tokens_per_page] makes the request's rows NaN.
  * ws: device workspace of slora_attn_workspace_size bytes, 256-byte aligned, zero-filled
  * once by the caller; calls of any shapes may share one, but must be ordered. Strides and pointers as for
  * slora_qkv. */
