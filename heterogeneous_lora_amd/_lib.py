@@ -96,6 +96,12 @@ class QKV(ctypes.Structure):
                 ("norm", _c_i32), ("eps", ctypes.c_float), ("q_weight", _vp), ("k_weight", _vp)]
 
 
+class KVRows(ctypes.Structure):
+    _fields_ = [("n_tokens", _c_i32), ("k", _vp), ("k_token_stride", _c_i64), ("k_head_stride", _c_i64),
+                ("v", _vp), ("v_token_stride", _c_i64), ("v_head_stride", _c_i64), ("k_slots", _vp),
+                ("v_slots", _vp)]
+
+
 class Attn(ctypes.Structure):
     _fields_ = [("n_q_heads", _c_i32), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
                 ("window", _c_i32), ("slopes", _vp), ("prefix_len", _vp), ("k_table", _vp),
@@ -178,6 +184,12 @@ def load(path: str = LIB_PATH):
         "slora_attn_workspace_size": ([P, P, I, P], I),
         "slora_attn_decode": ([P, P, P, _c_i64, P], I),
         "slora_attn_prefill": ([P, P, P, I, P, _c_i64, P], I),
+        "slora_kv4_token_bytes": ([I, I, P], I),
+        "slora_kv4_write": ([P, P, P], I),
+        "slora_kv4_read": ([P, P, P], I),
+        "slora_attn4_workspace_size": ([P, P, I, P], I),
+        "slora_attn4_decode": ([P, P, P, _c_i64, P], I),
+        "slora_attn4_prefill": ([P, P, P, I, P, _c_i64, P], I),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -591,9 +603,42 @@ def bind_attn_prefill(kv: KV, attn: Attn, q_offsets: int, n_tokens: int, ws: int
                   (kv, attn))
 
 
+def kv4_token_bytes(n_kv_heads: int, head_dim: int) -> int:
+    n = _c_i64()
+    _check(load().slora_kv4_token_bytes(n_kv_heads, head_dim, ctypes.byref(n)), "kv4_token_bytes")
+    return n.value
+
+
+def bind_kv4_write(kv: KV, qkv: QKV, stream: int):
+    return _bound("kv4_write", (ctypes.byref(kv), ctypes.byref(qkv), _vp(stream)), (kv, qkv))
+
+
+def bind_kv4_read(kv: KV, rows: KVRows, stream: int):
+    return _bound("kv4_read", (ctypes.byref(kv), ctypes.byref(rows), _vp(stream)), (kv, rows))
+
+
+def attn4_workspace_size(kv: KV, attn: Attn, n_tokens: int) -> int:
+    n = _c_i64()
+    _check(load().slora_attn4_workspace_size(ctypes.byref(kv), ctypes.byref(attn), n_tokens,
+                                             ctypes.byref(n)), "attn4_workspace_size")
+    return n.value
+
+
+def bind_attn4_decode(kv: KV, attn: Attn, ws: int, ws_bytes: int, stream: int):
+    return _bound("attn4_decode", (ctypes.byref(kv), ctypes.byref(attn), _vp(ws), _c_i64(ws_bytes),
+                                   _vp(stream)), (kv, attn))
+
+
+def bind_attn4_prefill(kv: KV, attn: Attn, q_offsets: int, n_tokens: int, ws: int, ws_bytes: int,
+                       stream: int):
+    return _bound("attn4_prefill", (ctypes.byref(kv), ctypes.byref(attn), _vp(q_offsets),
+                                    _c_i32(n_tokens), _vp(ws), _c_i64(ws_bytes), _vp(stream)),
+                  (kv, attn))
+
+
 KERNELS = ["mbgmv_shrink", "mbgmv_expand", "sgmv_shrink", "sgmv_expand", "mbgmv_fused", "gather",
            "fetch", "sgmv_fused", "mixed_fused", "multi_fused", "kv_tables", "kv_write", "attn_decode",
-           "attn_prefill"]
+           "attn_prefill", "kv4_write", "kv4_read", "attn4_decode", "attn4_prefill"]
 
 
 def timing_enable(on: bool):

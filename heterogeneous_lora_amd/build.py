@@ -24,7 +24,8 @@ ARCH = "gfx950"
 
 HOST_SRCS = ["pool.cpp", "plan.cpp", "api.cpp", "sched.cpp", "kv.cpp"]
 DEVICE_SRCS = ["mbgmv.hip", "sgmv.hip", "fetch.hip", "noalloc.hip", "gather.hip",
-               "kv_tables.hip", "kv_write.hip", "attn_decode.hip", "attn_prefill.hip"]
+               "kv_tables.hip", "kv_write.hip", "attn_decode.hip", "attn_prefill.hip",
+               "kv4_write.hip", "kv4_read.hip", "attn4_decode.hip", "attn4_prefill.hip"]
 
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function",
           f"-I{INCLUDE}", f"-I{CSRC}", "-D__HIP_PLATFORM_AMD__=1"]

@@ -22,6 +22,7 @@ struct alignas(16) AttnFill {
   uint16_t zero[256];
   uint16_t nan_f16[256];
   uint16_t nan_bf16[256];
+  uint8_t nan_steps[16];  // of a cache in 4 bits
 };
 constexpr AttnFill make_attn_fill() {
   AttnFill f{};
@@ -30,6 +31,7 @@ constexpr AttnFill make_attn_fill() {
     f.nan_f16[i] = 0x7E00;
     f.nan_bf16[i] = 0x7FC0;
   }
+  for (int i = 0; i < 16; ++i) f.nan_steps[i] = 255;
   return f;
 }
 __device__ AttnFill kAttnFill = make_attn_fill();

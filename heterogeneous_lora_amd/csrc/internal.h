@@ -263,6 +263,19 @@ inline void divisor(int32_t d, uint32_t* magic, uint32_t* shift) {
   *magic = (uint32_t)((uint64_t(1) << (31 + l)) / (uint32_t)d + 1);
   *shift = (uint32_t)(l - 1);
 }
+// A token of a cache in 4 bits (slora.h): the heads' codes, from steps_at on their steps, a head's
+// `step_bytes` apart; token_bytes in all.
+struct Kv4Layout {
+  int32_t groups, step_bytes, steps_at, token_bytes;
+};
+inline Kv4Layout kv4_layout(int32_t hk, int32_t D) {
+  Kv4Layout l;
+  l.groups = (D + 31) / 32;
+  l.step_bytes = l.groups <= 2 ? l.groups : l.groups <= 4 ? 4 : 8;
+  l.steps_at = hk * 16 * l.groups;
+  l.token_bytes = (l.steps_at + hk * l.step_bytes + 15) / 16 * 16;
+  return l;
+}
 // One attention call as the kernels see it (checked by kv.cpp). Strides in elements.
 struct AttnArgs {
   const uint16_t* pool;
@@ -294,6 +307,8 @@ struct AttnArgs {
                             // one a row tile, at most (0: tiles stay whole)
   int32_t part_waves;       // prefill: waves of a row tile that can hold rows
   int32_t wg_heads;         // decode: KV heads of a workgroup (1, 2 or 4)
+  Kv4Layout kv4;            // a cache in 4 bits
+  int32_t xcd_log2;         // decode of 4 bits: 3 where chunks go round the XCDs, else 0
 };
 // Floats of one row's partial result: max, sum, and the head's dimensions.
 inline int64_t attn_part_floats(int32_t D) { return D + 2; }
@@ -332,6 +347,10 @@ hipError_t launch_attn_decode(const AttnArgs& a, int32_t dtype, hipStream_t s, c
 hipError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, hipStream_t s, const LaunchEvents& ev);
 hipError_t launch_kv_tables(const slora_kv& kv, const slora_kv_step& st, hipStream_t s, const LaunchEvents& ev);
 hipError_t launch_kv_write(const slora_kv& kv, const slora_qkv& w, hipStream_t s, const LaunchEvents& ev);
+hipError_t launch_kv4_write(const slora_kv& kv, const slora_qkv& w, hipStream_t s, const LaunchEvents& ev);
+hipError_t launch_kv4_read(const slora_kv& kv, const slora_kv_rows& r, hipStream_t s, const LaunchEvents& ev);
+hipError_t launch_attn4_decode(const AttnArgs& a, int32_t dtype, hipStream_t s, const LaunchEvents& ev);
+hipError_t launch_attn4_prefill(const AttnArgs& a, int32_t dtype, hipStream_t s, const LaunchEvents& ev);
 // One call's launches, timed as kernel id `kernel` while kernel timing is on (api.cpp).
 // `launch` is called before these return, so it is passed by address: a call allocates nothing.
 hipError_t timed_call(int kernel, hipStream_t s, hipError_t (*launch)(const void*, const LaunchEvents&), const void* arg);

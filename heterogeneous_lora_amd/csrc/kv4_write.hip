@@ -1,0 +1,212 @@
+// Per-head norm of q and k, rotary positions, and K and V to their cache slots in 4 bits, in one
+// pass over the new tokens' projections (slora_kv4_write).
+//
+//   step = RN(max |x| / 6) over 32 dimensions,   code = the level nearest to x / step
+//
+// Heads are held as in kv_write_dev.h; q is what slora_kv_write makes of it. A group's largest
+// magnitude is that of its pieces, which travel between the lanes of a head through LDS.
+//
+// A code is a decision: two ways of rounding K that differ in the last of 32 bits would now and
+// then pick another level, a sixth of the group's range away. So K's norm, rotation, step and
+// quotient are in 64 bits, which the vector unit does at the rate of 32, and x / step is
+// corrected and cut to a float in a way that no border is met or passed: the level is that of the
+// exactly computed value, unless 2^-50 of it decides. (V has no arithmetic before its
+// step, and is exact.)
+#include "kv_write_dev.h"
+
+namespace slora {
+namespace {
+
+struct Write4 {
+  WriteArgs a;
+  Kv4Layout lay;
+};
+
+// Upper bits of the f16 value nearest to `most` / 6 among those with 3 bits behind the leading
+// one: a group's step byte. 226 is the largest whose 6-fold is finite in f16.
+constexpr int kMaxStep = 226, kNanStep = 255;
+__device__ __forceinline__ int step_byte(double most) {
+  if (!(most < INFINITY)) return kNanStep;
+  const double x = most / 6.0;
+  // multiples of 2^(e - 3), e = the exponent, -14 at least
+  const int e = max((int)((__double2hiint(x) >> 20) & 0x7ff) - 1023, -14);
+  if (e > 14) return kMaxStep;
+  const int n = (int)rint(ldexp(x, 3 - e));  // 0 .. 16
+  return min((e + 14) * 8 + n, kMaxStep);    // n = 16 carries into the exponent
+}
+__device__ __forceinline__ float step_value(int byte) {
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)(byte << 7));
+}
+
+// x / step, as a float on the same side of every level's border: cut off towards zero and made
+// odd if anything was lost (the borders have few bits, so no odd float is one).
+__device__ __forceinline__ float quotient(double x, double step, double inv) {
+  double t = x * inv;
+  t = fma(fma(-t, step, x), inv, t);
+  const float f = (float)t;
+  const double lost = fabs(t) - fabs((double)f);
+  const int bits = __float_as_int(f);
+  return __int_as_float(lost == 0.0 ? bits : (lost < 0.0 ? bits - 1 : bits) | 1);
+}
+__device__ __forceinline__ float quotient(float x, float step, float inv) {
+  const float t = x * inv;
+  return fmaf(fmaf(-t, step, x), inv, t);
+}
+
+// Codes of a piece, 4 bits each.
+template <int V, typename F>
+__device__ __forceinline__ uint32_t codes_of(const F (&x)[V], int byte) {
+  const float step = byte < kNanStep ? step_value(byte) : 0.f;
+  const F s = (F)step, inv = step == 0.f ? (F)0 : (F)1 / s;
+  uint32_t w = 0;
+  float t[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) t[e] = fminf(fmaxf(step == 0.f ? 0.f : quotient(x[e], s, inv), -6.f), 6.f);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[0], t[1], 1.0f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[2], t[3], 1.0f, 1);
+  if constexpr (V == 8) {
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[4], t[5], 1.0f, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[6], t[7], 1.0f, 3);
+  }
+  return w;
+}
+
+// V, G, INTER as for slora_kv_write.
+template <int DT, int V, int G, bool INTER>
+__global__ __launch_bounds__(kThreads) void kv4_write_kernel(Write4 b) {
+  const WriteArgs& a = b.a;
+  const Kv4Layout& lay = b.lay;
+  __shared__ double2 angle[kAngles];
+  __shared__ double sm_most[kThreads * 2];  // largest magnitudes of the pieces, by group of lanes
+  const int tid = (int)threadIdx.x;
+  const int tok0 = (int)blockIdx.x * a.tpw, n_tok = min(a.tpw, a.n_tok - tok0);
+  const int pairs = a.pairs;
+  for (int i = tid; i < n_tok * pairs; i += kThreads) {
+    const int t = i / pairs, c = i - t * pairs;
+    double f = (double)a.pos[tok0 + t] * a.turns[c];
+    f -= rint(f);
+    double sn, cs;
+    sincospi(2.0 * f, &sn, &cs);
+    angle[i] = make_double2(cs * a.cs, sn * a.cs);
+  }
+  __syncthreads();
+
+  const Place at = place_of<V, INTER>(a, tid % G);
+  double* const most = sm_most + tid / G * 2 * G;
+
+  // What the cache holds of the lane's pieces x and y, to the head at `dst`.
+  auto put = [&](uint8_t* token, int hh, const auto& x, const auto& y) {
+    double mx = 0.0, my = 0.0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      mx = fmax(mx, fabs((double)x[e]));  // (passes over NaN)
+      my = fmax(my, fabs((double)y[e]));
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if (x[e] != x[e]) mx = INFINITY;
+      if (y[e] != y[e]) my = INFINITY;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    most[at.c0] = mx;
+    most[at.c1] = my;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    constexpr int kIn = 32 / V;  // pieces of a group of 32
+    auto store = [&](int c, const auto& z) {
+      const int group = c / kIn;
+      if (group >= lay.groups) return;
+      double m = 0.0;
+#pragma unroll
+      for (int i = 0; i < kIn; ++i) m = fmax(m, most[group * kIn + i]);
+      const int byte = step_byte(m);
+      const uint32_t w = codes_of<V>(z, byte);
+      const int p = c * V / 8, word = (p & 3) * lay.groups + (p >> 2);  // its 8 dimensions' place
+      uint8_t* to = token + hh * 16 * lay.groups + word * 4;
+      if constexpr (V == 8) *reinterpret_cast<uint32_t*>(to) = w;
+      else *reinterpret_cast<uint16_t*>(to + (c & 1) * 2) = (uint16_t)w;
+      if (c % kIn == 0) token[lay.steps_at + hh * lay.step_bytes + group] = (uint8_t)byte;
+    };
+    store(at.c0, x);
+    store(at.c1, y);
+  };
+
+  const int heads = a.hq + 2 * a.hk;
+  const int h_begin = (int)blockIdx.y * a.heads_y, h_end = min(h_begin + a.heads_y, heads);
+  const int n_heads = h_end - h_begin;
+  for (int i = tid / G; i < n_tok * n_heads; i += kThreads / G) {
+    const int t = i / n_heads, h = h_begin + i - t * n_heads;
+    const int64_t tok = tok0 + t;
+    if (a.pos[tok] < 0) continue;
+    const bool is_q = h < a.hq, is_v = h >= a.hq + a.hk;
+    const int hh = is_q ? h : is_v ? h - a.hq - a.hk : h - a.hq;
+    const uint16_t* src = is_q ? a.q.p + tok * a.q.ts + hh * a.q.hs
+                          : is_v ? a.v.p + tok * a.v.ts + hh * a.v.hs
+                                 : a.k.p + tok * a.k.ts + hh * a.k.hs;
+    uint8_t* token = nullptr;
+    if (!is_q) {
+      const int64_t slot = (is_v ? a.vs : a.ks)[tok];
+      const int64_t page = (slot >> 32) ? slot / a.tpp : (int64_t)((uint32_t)slot / (uint32_t)a.tpp);
+      if (slot < 0 || page >= a.n_pages) continue;
+      token = (uint8_t*)(a.pool + page * a.P) + (slot - page * a.tpp) * lay.token_bytes;
+    }
+    Piece<V> r0{}, r1{};
+    if (at.has0) r0 = load<V>(src + at.c0 * V);
+    if (at.has1) r1 = load<V>(src + at.c1 * V);
+    float x[V], y[V];
+    unpack<DT, V>(r0, x);
+    unpack<DT, V>(r1, y);
+    const double2* ang = angle + t * pairs;
+    if (is_q) {
+      norm_and_turn<DT, V, G, INTER>(a, ang, a.qw, at, x, y);
+      uint16_t* dst = a.qo + tok * a.ots + hh * a.ohs;
+      if (at.has0) store<V>(dst + at.c0 * V, pack<DT, V>(x));
+      if (at.has1) store<V>(dst + at.c1 * V, pack<DT, V>(y));
+    } else if (is_v) {
+      put(token, hh, x, y);
+    } else {
+      double kx[V], ky[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        kx[e] = x[e];
+        ky[e] = y[e];
+      }
+      norm_and_turn<DT, V, G, INTER>(a, ang, a.kw, at, kx, ky);
+      put(token, hh, kx, ky);
+    }
+  }
+}
+
+template <int DT, int V, int G>
+void launch_one(bool inter, const Write4& a, dim3 grid, hipStream_t s, const LaunchEvents& ev) {
+  if (inter)
+    hipExtLaunchKernelGGL((kv4_write_kernel<DT, V, G, true>), grid, dim3(kThreads), 0, s, ev.start, ev.stop, 0, a);
+  else
+    hipExtLaunchKernelGGL((kv4_write_kernel<DT, V, G, false>), grid, dim3(kThreads), 0, s, ev.start, ev.stop, 0, a);
+}
+
+template <int DT>
+void launch_dt(const Plan& p, const Write4& a, hipStream_t s, const LaunchEvents& ev) {
+  if (p.v == 8) {
+    if (p.g <= 4) launch_one<DT, 8, 4>(p.inter, a, p.grid, s, ev);
+    else if (p.g <= 8) launch_one<DT, 8, 8>(p.inter, a, p.grid, s, ev);
+    else launch_one<DT, 8, 16>(p.inter, a, p.grid, s, ev);
+  } else {
+    if (p.g <= 8) launch_one<DT, 4, 8>(p.inter, a, p.grid, s, ev);
+    else if (p.g <= 16) launch_one<DT, 4, 16>(p.inter, a, p.grid, s, ev);
+    else launch_one<DT, 4, 32>(p.inter, a, p.grid, s, ev);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_kv4_write(const slora_kv& kv, const slora_qkv& w, hipStream_t s, const LaunchEvents& ev) {
+  const Plan p = plan_write(kv, w);
+  if ((int64_t)p.grid.x * kThreads >= kMaxThreads) return hipErrorInvalidConfiguration;
+  const Write4 a = {p.a, kv4_layout(kv.n_kv_heads, kv.head_dim)};
+  if (kv.dtype == SLORA_F16) launch_dt<SLORA_F16>(p, a, s, ev);
+  else launch_dt<SLORA_BF16>(p, a, s, ev);
+  return hipGetLastError();
+}
+
+}  // namespace slora

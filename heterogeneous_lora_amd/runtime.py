@@ -342,7 +342,8 @@ def _opt(t: Optional[torch.Tensor]):
 
 
 class KVCache:
-    """The pool's KV pages as the attention operators see them (slora_kv).
+    """The pool's KV pages as the attention operators see them (slora_kv). bits: of a cached value,
+    16 (the cache's type) or 4 (slora.h, "KV cache in 4 bits"; dtype is then that of q, k, v and out).
 
     Each bind_* method checks shapes and types, marshals one call's arguments once and
     returns a no-argument callable; the method of the same name without bind_ makes the call
@@ -351,7 +352,9 @@ class KVCache:
     made, zeroed and, with the bound call, freed on that stream."""
 
     def __init__(self, pool: Optional[torch.Tensor], n_pages: int, page_elems: int = 0, dtype: str = "f16",
-                 n_kv_heads: int = 1, head_dim: int = 8, tokens_per_page: int = 1):
+                 n_kv_heads: int = 1, head_dim: int = 8, tokens_per_page: int = 1, bits: int = 16):
+        if bits not in (4, 16):
+            raise ValueError(f"bits: expected 4 or 16, got {bits}")
         if pool is not None and pool.numel() * pool.element_size() < 2 * n_pages * page_elems:
             raise ValueError(f"pool holds fewer than {n_pages} pages of {page_elems} elements")
         if pool is not None:
@@ -361,6 +364,12 @@ class KVCache:
         self.pool, self.n_pages, self.page_elems, self.dtype = pool, n_pages, page_elems, dtype
         self.n_kv_heads, self.head_dim, self.tokens_per_page = n_kv_heads, head_dim, tokens_per_page
         self.device = None if pool is None else pool.device
+        self.bits = bits
+        four = bits == 4
+        self._bind_write = _lib.bind_kv4_write if four else _lib.bind_kv_write
+        self._bind_decode = _lib.bind_attn4_decode if four else _lib.bind_attn_decode
+        self._bind_prefill = _lib.bind_attn4_prefill if four else _lib.bind_attn_prefill
+        self.workspace_size = _lib.attn4_workspace_size if four else _lib.attn_workspace_size
 
     def _kv(self, n_requests: int = 0, max_blocks: int = 0) -> _lib.KV:
         return _lib.KV(_opt(self.pool), self.n_pages, self.page_elems, _lib.DTYPES[self.dtype],
@@ -400,7 +409,7 @@ class KVCache:
     def tables(self, *args, **kw):
         self.bind_tables(*args, **kw)()
 
-    # -- norm, rotation, store (slora_kv_write)
+    # -- norm, rotation, store (slora_kv_write, slora_kv4_write)
     def bind_write(self, q: torch.Tensor, k: Optional[torch.Tensor], v: Optional[torch.Tensor],
                    q_out: torch.Tensor, position: torch.Tensor, k_slots: Optional[torch.Tensor],
                    v_slots: Optional[torch.Tensor], rope: Optional[Rope] = None, norm: bool = False,
@@ -429,14 +438,39 @@ class KVCache:
             if t is not None:
                 _expect(name, t, TORCH_DTYPES[self.dtype], (self.head_dim,), q.device)
         w.norm, w.eps, w.q_weight, w.k_weight = int(norm), eps, _opt(q_weight), _opt(k_weight)
-        call = _lib.bind_kv_write(self._kv(), w, self._stream(q, stream))
+        call = self._bind_write(self._kv(), w, self._stream(q, stream))
         call.tensors = (self.pool, q, k, v, q_out, position, k_slots, v_slots, rope, q_weight, k_weight)
         return call
 
     def write(self, *args, **kw):
         self.bind_write(*args, **kw)()
 
-    # -- attention (slora_attn_decode, slora_attn_prefill)
+    # -- K and V of tokens in 16 bits (slora_kv4_read)
+    def bind_read(self, k: Optional[torch.Tensor], v: Optional[torch.Tensor], k_slots: Optional[torch.Tensor],
+                  v_slots: Optional[torch.Tensor], stream: Optional[torch.cuda.Stream] = None):
+        if self.bits != 4:
+            raise ValueError("read: the cache's pages hold 16-bit vectors already")
+        if (k is None and v is None) or (k is None) != (k_slots is None) or (v is None) != (v_slots is None):
+            raise ValueError("read: k with k_slots, v with v_slots, or both")
+        r = _lib.KVRows()
+        n = (k if k is not None else v).shape[0]
+        r.n_tokens = n
+        if k is not None:
+            r.k, r.k_token_stride, r.k_head_stride = self._rows("k", k, n, self.n_kv_heads)
+            _expect("k_slots", k_slots, torch.int64, (n,), k.device)
+            r.k_slots = k_slots.data_ptr()
+        if v is not None:
+            r.v, r.v_token_stride, r.v_head_stride = self._rows("v", v, n, self.n_kv_heads)
+            _expect("v_slots", v_slots, torch.int64, (n,), v.device)
+            r.v_slots = v_slots.data_ptr()
+        call = _lib.bind_kv4_read(self._kv(), r, self._stream(k if k is not None else v, stream))
+        call.tensors = (self.pool, k, v, k_slots, v_slots)
+        return call
+
+    def read(self, *args, **kw):
+        self.bind_read(*args, **kw)()
+
+    # -- attention (slora_attn_decode, slora_attn_prefill and their forms of 4 bits)
     def _attn(self, q, out, k_table, v_table, seq_len, scale, softcap, window, slopes, prefix_len, lse):
         n_req, max_blocks = k_table.shape
         a = _lib.Attn()
@@ -459,7 +493,7 @@ class KVCache:
         return a, self._kv(n_req, max_blocks), (self.pool, q, out, k_table, v_table, seq_len, slopes, prefix_len, lse)
 
     def _ws(self, kv, a, n_tokens, ws, device, stream):
-        need = _lib.attn_workspace_size(kv, a, n_tokens)
+        need = self.workspace_size(kv, a, n_tokens)
         if ws is not None:
             _on_gpu("ws", ws, device)
             if not ws.is_contiguous():
@@ -478,7 +512,7 @@ class KVCache:
         a, kv, tensors = self._attn(q, out, k_table, v_table, seq_len, scale, softcap, window, slopes,
                                     prefix_len, lse)
         ws = self._ws(kv, a, 0, ws, q.device, stream)
-        call = _lib.bind_attn_decode(kv, a, ws.data_ptr(), ws.nbytes, self._stream(q, stream))
+        call = self._bind_decode(kv, a, ws.data_ptr(), ws.nbytes, self._stream(q, stream))
         call.tensors = tensors + (ws,)
         return call
 
@@ -494,8 +528,8 @@ class KVCache:
                                     prefix_len, lse)
         _expect("q_offsets", q_offsets, torch.int32, (k_table.shape[0] + 1,), q.device)
         ws = self._ws(kv, a, q.shape[0], ws, q.device, stream)
-        call = _lib.bind_attn_prefill(kv, a, q_offsets.data_ptr(), q.shape[0], ws.data_ptr(), ws.nbytes,
-                                      self._stream(q, stream))
+        call = self._bind_prefill(kv, a, q_offsets.data_ptr(), q.shape[0], ws.data_ptr(), ws.nbytes,
+                                  self._stream(q, stream))
         call.tensors = tensors + (q_offsets, ws)
         return call
 
@@ -529,7 +563,7 @@ class AttentionLoop(ServingLoop):
         """One workspace for every call of the loop, grown as steps need it. calls: (requests,
         prompt tokens) of each, 0 tokens for slora_attn_decode."""
         a = _lib.Attn(n_q_heads=self.n_q_heads)
-        need = max(_lib.attn_workspace_size(self.cache._kv(r, self.max_len), a, n) for r, n in calls)
+        need = max(self.cache.workspace_size(self.cache._kv(r, self.max_len), a, n) for r, n in calls)
         if self.ws is None or self.ws.numel() < need:
             self.ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
         return self.ws

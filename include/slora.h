@@ -622,6 +622,60 @@ int slora_attn_decode(const slora_kv* kv, const slora_attn* attn, void* ws, int6
 int slora_attn_prefill(const slora_kv* kv, const slora_attn* attn, const int32_t* q_offsets,
                        int32_t n_tokens, void* ws, int64_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ KV cache in 4 bits
+ * The calls above with a cache of 4 bits a value and 8 for the step that 32 of them share: 68
+ * bytes for a head of 128 where 16 bits take 256. The arguments and their checks are the same;
+ * of a page (page_elems 16-bit elements, 2 page_elems bytes) token i's part begins at byte i *
+ * token_bytes (slora_kv4_token_bytes), tokens_per_page * token_bytes <= 2 * page_elems. dtype is
+ * the type of q, k, v, out and the norm weights.
+ *
+ * A head's vector is cut into G = ceil(head_dim / 32) groups of 32 dimensions, the last one filled
+ * up with zeros. A value is step * level, level one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives:
+ *   step = max |x| of the group / 6, rounded to the nearest number of 3 bits behind the leading
+ *          one, 10240 at most (then 6 * step is finite in f16), multiples of 2^-17 below 2^-14;
+ *   level: the one nearest to x / step (of two equally near the one with the even number).
+ * Both are decided from the exactly computed x (K after norm and rotation: in 64 bits). A group
+ * that holds an infinity or NaN reads as NaN; values beyond 61440 read as 61440. step * level is
+ * held by f16 and bf16 exactly, so slora_kv4_read gives what the attention calls see.
+ *
+ * Bytes of a token's K (or V): for every KV head its codes, 16 G bytes; then for every KV head
+ * its G steps, a byte each, G rounded up to 1, 2, 4 or 8 bytes; the whole rounded up to 16. Codes
+ * of dimensions 32 c + 8 g .. + 7 are the 4 bytes from byte 4 (g G + c) of the head's on,
+ * dimension 32 c + 8 g + e in bits 4 e of that word: the level's number, 8 added if negative. A
+ * step's byte is the upper 8 of the 15 bits below the sign of its f16 value; 255: a NaN. (227 to
+ * 254 are not written; what they read as is not defined.) */
+int slora_kv4_token_bytes(int32_t n_kv_heads, int32_t head_dim, int64_t* bytes);
+
+/* slora_kv_write, K and V stored in 4 bits. */
+int slora_kv4_write(const slora_kv* kv, const slora_qkv* qkv, void* stream);
+
+/* K and V of tokens in 16 bits: row t of k is the K at k_slots[t], row t of v the V at v_slots[t].
+ * A row whose slot is outside the pool is left as it is. k or v NULL: the other alone (its slots
+ * are not used). Strides and pointers as for slora_qkv; n_requests and max_blocks are not used. */
+typedef struct {
+  int32_t n_tokens;
+  void* k; /* [n_tokens][n_kv_heads][head_dim] or NULL */
+  int64_t k_token_stride, k_head_stride;
+  void* v;
+  int64_t v_token_stride, v_head_stride;
+  const int64_t* k_slots; /* [n_tokens] */
+  const int64_t* v_slots;
+} slora_kv_rows;
+int slora_kv4_read(const slora_kv* kv, const slora_kv_rows* rows, void* stream);
+
+/* The attention calls over a cache in 4 bits: what they give over the values slora_kv4_read
+ * gives, K, V and the weights of the product with V held in f16 whatever dtype is (bf16 q is
+ * brought to f16 by a power of two a row: exact down to 2^-32 of the row's largest element). The
+ * weights exp(s - max) are in slora_attn4_decode with f16 q sums of two f16 values (2^-21 of a
+ * weight is lost), otherwise rounded to f16 once (2^-11 of a weight; 2^-32 of the largest if that
+ * is more). A page id outside the pool reads as NaN. Workspaces as for slora_attn_*, which may
+ * share them. */
+int slora_attn4_workspace_size(const slora_kv* kv, const slora_attn* attn, int32_t n_tokens, int64_t* bytes);
+int slora_attn4_decode(const slora_kv* kv, const slora_attn* attn, void* ws, int64_t ws_bytes, void* stream);
+int slora_attn4_prefill(const slora_kv* kv, const slora_attn* attn, const int32_t* q_offsets, int32_t n_tokens,
+                        void* ws, int64_t ws_bytes, void* stream);
+
 /* Kernel timing for benchmarks. While enabled (on != 0), every kernel a compute
  * call launches carries two HIP events that the launch itself records on the call's
  * stream when the kernel starts and when it ends (hipExtLaunchKernel), so a timed
@@ -646,7 +700,11 @@ int slora_attn_prefill(const slora_kv* kv, const slora_attn* attn, const int32_t
 #define SLORA_K_KV_WRITE 11
 #define SLORA_K_ATTN_DECODE 12  /* the launches of one slora_attn_decode, as one interval */
 #define SLORA_K_ATTN_PREFILL 13 /* the launches of one slora_attn_prefill, as one interval */
-#define SLORA_K_COUNT 14
+#define SLORA_K_KV4_WRITE 14
+#define SLORA_K_KV4_READ 15
+#define SLORA_K_ATTN4_DECODE 16  /* as SLORA_K_ATTN_DECODE */
+#define SLORA_K_ATTN4_PREFILL 17 /* as SLORA_K_ATTN_PREFILL */
+#define SLORA_K_COUNT 18
 int slora_timing_enable(int32_t on);
 
 /* Waits for the recorded events, then writes per kernel id the number of timed
