@@ -9,38 +9,45 @@ namespace dev {
 
 constexpr int kMaxStep = 226;  // the largest step byte of numbers
 
+// Where the codes of keys whose page is outside the pool are read (their steps are NaN): as
+// long as 16 of the largest heads' codes.
+__device__ uint4 kNoCodes[128];
+
 // (A factor that has overflowed would make NaN of a score of 0.)
 __device__ __forceinline__ float finite(float x) { return fminf(fmaxf(x, -3.402823466e38f), 3.402823466e38f); }
 
-// Words (4-byte aligned) from an address.
+// Loads from an address. (Said to be of global memory: the compiler cannot tell, and a load that
+// may be of LDS is waited for with everything else that is on its way.)
+#define SLORA_GLOBAL __attribute__((address_space(1)))
 typedef uint32_t words2 __attribute__((ext_vector_type(2), aligned(4)));
 typedef uint32_t words4 __attribute__((ext_vector_type(4), aligned(4)));
+// Words, 4-byte aligned.
 template <int N>
 __device__ __forceinline__ void load_words(uint64_t from, uint32_t (&w)[N]) {
-  const uint32_t* p = (const uint32_t*)from;
+  const SLORA_GLOBAL uint32_t* p = (const SLORA_GLOBAL uint32_t*)from;
 #pragma unroll
   for (int i = 0; i + 4 <= N; i += 4) {
-    const words4 x = *reinterpret_cast<const words4*>(p + i);
+    const words4 x = *(const SLORA_GLOBAL words4*)(p + i);
     w[i] = x[0]; w[i + 1] = x[1]; w[i + 2] = x[2]; w[i + 3] = x[3];
   }
   if constexpr (N % 4 >= 2) {
-    const words2 x = *reinterpret_cast<const words2*>(p + N / 4 * 4);
+    const words2 x = *(const SLORA_GLOBAL words2*)(p + N / 4 * 4);
     w[N / 4 * 4] = x[0]; w[N / 4 * 4 + 1] = x[1];
   }
   if constexpr (N % 2) w[N - 1] = p[N - 1];
 }
-// A head's steps, a byte each (what lies behind them in the words is not a step).
+// A head's steps, a byte each.
 template <int G, int N>
 __device__ __forceinline__ void load_steps(uint64_t from, uint32_t (&w)[N]) {
-  if constexpr (G == 1) w[0] = *(const uint8_t*)from;
-  else if constexpr (G == 2) w[0] = *(const uint16_t*)from;
+  if constexpr (G == 1) w[0] = *(const SLORA_GLOBAL uint8_t*)from;
+  else if constexpr (G == 2) w[0] = *(const SLORA_GLOBAL uint16_t*)from;
   else load_words<N>(from, w);
 }
 // The codes of 8 (or 4, in the low half) dimensions.
 template <int D>
 __device__ __forceinline__ uint32_t load_codes(uint64_t from) {
-  if constexpr (D == 8) return *(const uint32_t*)from;
-  else return *(const uint16_t*)from;
+  if constexpr (D == 8) return *(const SLORA_GLOBAL uint32_t*)from;
+  else return *(const SLORA_GLOBAL uint16_t*)from;
 }
 
 // A key's codes and steps (of KV head `head`); good: its page is in the pool.

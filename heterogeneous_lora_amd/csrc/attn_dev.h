@@ -22,7 +22,7 @@ struct alignas(16) AttnFill {
   uint16_t zero[256];
   uint16_t nan_f16[256];
   uint16_t nan_bf16[256];
-  uint8_t nan_steps[16];  // of a cache in 4 bits
+  uint8_t nan_steps[64];  // of a cache in 4 bits
 };
 constexpr AttnFill make_attn_fill() {
   AttnFill f{};
@@ -31,7 +31,7 @@ constexpr AttnFill make_attn_fill() {
     f.nan_f16[i] = 0x7E00;
     f.nan_bf16[i] = 0x7FC0;
   }
-  for (int i = 0; i < 16; ++i) f.nan_steps[i] = 255;
+  for (int i = 0; i < 64; ++i) f.nan_steps[i] = 255;
   return f;
 }
 __device__ AttnFill kAttnFill = make_attn_fill();
@@ -219,6 +219,25 @@ __device__ __forceinline__ void put_pair(float* p, float x, float y) {
 __device__ __forceinline__ float part_weight(float m_part, float m) {
   return m_part == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m_part - m);
 }
+
+// 16 bytes of every lane from its address to LDS: lane l's land at lds + 16 l. Written out
+// because the compiler, which cannot tell the tile being filled from the one being read,
+// would wait for these loads before every read of LDS; landed() is the wait.
+__device__ __forceinline__ void load_to_lds(uint64_t from, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "{m0}"(lds), "v"(from) : "memory");
+}
+__device__ __forceinline__ void load_word_to_lds(uint64_t from, uint32_t lds) {  // 4 bytes, at lds + 4 l
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, off" :: "{m0}"(lds), "v"(from) : "memory");
+}
+// All but the last N loads have.
+template <int N>
+__device__ __forceinline__ void some_landed() {
+  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
+}
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+typedef __attribute__((address_space(3))) void lds_void;
+__device__ __forceinline__ uint32_t lds_offset(const void* p) { return (uint32_t)(uintptr_t)(lds_void*)p; }
 
 }  // namespace dev
 }  // namespace slora

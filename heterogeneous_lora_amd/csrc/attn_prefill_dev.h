@@ -109,17 +109,6 @@ __device__ __forceinline__ T settled(T x) {
   return x;
 }
 
-// 16 bytes of every lane from its address to LDS: lane l's land at lds + 16 l. Written out
-// because the compiler, which cannot tell the tile being filled from the one being read,
-// would wait for these loads before every read of LDS; landed() is the wait.
-__device__ __forceinline__ void load_to_lds(uint64_t from, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" :: "{m0}"(lds), "v"(from) : "memory");
-}
-__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-typedef __attribute__((address_space(3))) void lds_void;
-__device__ __forceinline__ uint32_t lds_offset(const void* p) { return (uint32_t)(uintptr_t)(lds_void*)p; }
-
 // 16 bytes `off` past an LDS offset (a constant `off` is the instruction's).
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef const __attribute__((address_space(3))) char lds_bytes;
@@ -278,7 +267,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
         load_words<NC>(at, codes[j]);
       } else {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) codes[j][c] = ((const uint32_t*)at)[min(c, a.kv4.groups - 1)];
+        for (int c = 0; c < NC; ++c) codes[j][c] = ((const SLORA_GLOBAL uint32_t*)at)[min(c, a.kv4.groups - 1)];
       }
       const uint64_t st = index4(turn, j) >= keys.count ? zeros : k.good ? k.steps : (uint64_t)kAttnFill.nan_steps;
       if (NC == 2 && a.kv4.groups == 1) load_steps<1>(st, steps[j]);
@@ -595,7 +584,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
       const int j = keys.key(i);
       if constexpr (k4) {
         const Key4 k = key4_addr(a, vt[div_tpp(a, (uint32_t)j)], j, kv_head);
-        const uint8_t* st = (const uint8_t*)(k.good ? k.steps : (uint64_t)kAttnFill.nan_steps);
+        const SLORA_GLOBAL uint8_t* st = (const SLORA_GLOBAL uint8_t*)(k.good ? k.steps : (uint64_t)kAttnFill.nan_steps);
         const bool on = ((i <= see_hi) & (i >= see_lo)) | (i < prefix);
 #pragma unroll
         for (int d = 0; d < NC; ++d) {

@@ -308,7 +308,12 @@ struct AttnArgs {
   int32_t part_waves;       // prefill: waves of a row tile that can hold rows
   int32_t wg_heads;         // decode: KV heads of a workgroup (1, 2 or 4)
   Kv4Layout kv4;            // a cache in 4 bits
-  int32_t xcd_log2;         // decode of 4 bits: 3 where chunks go round the XCDs, else 0
+  // decode of 4 bits
+  int32_t wave_heads, wave_runs;  // KV heads of a wave, its runs of 32 keys
+  int32_t wg_units;         // waves of a workgroup on different heads
+  int32_t spans;            // into which all requests' keys are cut
+  int2* cut;                // [n_req]: the span a request begins in, the spans it is in
+  int32_t xcd_log2;         // 3 where spans go round the XCDs, else 0
 };
 // Floats of one row's partial result: max, sum, and the head's dimensions.
 inline int64_t attn_part_floats(int32_t D) { return D + 2; }
@@ -324,6 +329,44 @@ inline int32_t decode_units(int32_t n_req, int32_t hk, int32_t group) {
   return hk / decode_wg_heads(n_req, hk, group) * ((group + 15) / 16);
 }
 inline int32_t decode_chunks(int32_t units) { return (kDecodeTarget + units - 1) / units; }
+// The workspace begins with the counters: chunks aimed for x units (decode) or x hk
+// (prefill), at most kDecodeTarget + units, and hk + hq / 16 bounds units (hk <= 1024, hq <=
+// 16384).
+constexpr int64_t kAttnCounters = kDecodeTarget + 2048;
+constexpr int64_t kAttnCounterBytes = kAttnCounters * 4;
+// Decode of 4 bits, many keys: KV heads that a wave takes one after the other (with the query heads
+// that share them up to 16 rows), the runs of 32 keys that it takes at once, waves of a workgroup on
+// different heads, and into how many spans all requests' keys are cut (0: few keys, which go to
+// attn_decode_kernel).
+struct Decode4 {
+  int32_t heads, runs, wg_units, spans;
+};
+// Vectors of K that requests may have above which spans pay, us with spans and without: 64 requests
+// of up to 4096 keys, 8 heads (2.1 million) 92 and 91; 3 of 131072 (3.1) 119 and 128; 128 of 1024,
+// 32 heads (4.2) 92 and 123; 512 of 2048, 40 heads (42) 687 and 985; 16 of 512, 32 heads (0.3) 25
+// and 12.
+constexpr int64_t kDecode4Vectors = 2500000;
+constexpr int32_t kDecode4Spans = 512;  // two workgroups a CU (256: 974 us, 768: 801, 1024: 703)
+inline Decode4 decode4_plan(int32_t n_req, int32_t hk, int32_t group, int32_t head_dim, int32_t max_len, int32_t window) {
+  Decode4 d = {};
+  if ((int64_t)n_req * hk * (window && window < max_len ? window : max_len) < kDecode4Vectors) return d;
+  // a token's heads over the 4 waves of a workgroup (15 to a wave would leave some wave's steps in 5
+  // units of 16 bytes, more than 7 of heads above 128 too)
+  const int32_t most = group >= 16 ? 1 : 16 / group, row_groups = (group + 15) / 16;
+  const int32_t share = (hk + 3) / 4, room = head_dim > 128 ? 7 : 16;
+  d.heads = share < most ? share : most;
+  if (d.heads > room) d.heads = room;
+  if (d.heads == 15) d.heads = most > 15 ? 16 : 14;
+  const int64_t units = (int64_t)((hk + d.heads - 1) / d.heads) * row_groups;
+  d.wg_units = units >= 3 ? 4 : (int32_t)units;
+  // (the steps of more heads would not fit 32 bytes a key, of more than one 16)
+  const int32_t few = head_dim > 128 ? 3 : 5;
+  d.runs = d.heads > few || max_len < 1024 ? 1 : d.heads > 1 || head_dim > 128 ? 2 : 4;
+  // as many spans as fit the device at once, whole rounds of the XCDs
+  const int64_t groups = (units + d.wg_units - 1) / d.wg_units, spans = (kDecode4Spans + groups - 1) / groups;
+  d.spans = (int32_t)((spans + 7) / 8 * 8);
+  return d;
+}
 // Prefill: one part's floats, of one wave (NC pieces of 32 dimensions of 32 rows, in pairs of
 // 64 lanes, and the pair m, l); instances of NC; chunks past one a row tile.
 constexpr int32_t part_floats(int32_t nc) { return 128 * (nc * 8 + 1); }
@@ -338,11 +381,6 @@ inline int32_t prefill_chunks(int64_t n_tok, int32_t group, int32_t hk, int32_t 
 inline int32_t prefill_waves(int64_t n_tok, int32_t group) {
   return n_tok * group >= 128 ? 4 : (int32_t)((n_tok * group + 31) / 32);
 }
-// The workspace begins with the counters: chunks aimed for x units (decode) or x hk
-// (prefill), at most kDecodeTarget + units, and hk + hq / 16 bounds units (hk <= 1024, hq <=
-// 16384).
-constexpr int64_t kAttnCounters = kDecodeTarget + 2048;
-constexpr int64_t kAttnCounterBytes = kAttnCounters * 4;
 hipError_t launch_attn_decode(const AttnArgs& a, int32_t dtype, hipStream_t s, const LaunchEvents& ev);
 hipError_t launch_attn_prefill(const AttnArgs& a, int32_t dtype, hipStream_t s, const LaunchEvents& ev);
 hipError_t launch_kv_tables(const slora_kv& kv, const slora_kv_step& st, hipStream_t s, const LaunchEvents& ev);

@@ -115,7 +115,10 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(Write4 b) {
     constexpr int kIn = 32 / V;  // pieces of a group of 32
     auto store = [&](int c, const auto& z) {
       const int group = c / kIn;
-      if (group >= lay.groups) return;
+      if (group >= lay.groups) {  // a head's steps are filled up with zeros
+        if (c % kIn == 0 && group < lay.step_bytes) token[lay.steps_at + hh * lay.step_bytes + group] = 0;
+        return;
+      }
       double m = 0.0;
 #pragma unroll
       for (int i = 0; i < kIn; ++i) m = fmax(m, most[group * kIn + i]);

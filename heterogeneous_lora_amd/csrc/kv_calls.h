@@ -128,10 +128,17 @@ inline int check_heads(const char* what, int bits, const slora_kv* kv, const slo
   return SLORA_OK;
 }
 
-inline int64_t decode_workspace(const slora_kv* kv, const slora_attn* at) {
-  const int units = decode_units(kv->n_requests, kv->n_kv_heads, at->n_q_heads / kv->n_kv_heads);
-  return kAttnCounterBytes + ((int64_t)kv->n_requests + decode_chunks(units)) * at->n_q_heads *
-                                 attn_part_floats(kv->head_dim) * (int64_t)sizeof(float);
+inline int64_t decode4_cut_bytes(int32_t n_req) { return ((int64_t)n_req * 8 + 255) / 256 * 256; }
+
+inline int64_t decode_workspace(int bits, const slora_kv* kv, const slora_attn* at) {
+  const int group = at->n_q_heads / kv->n_kv_heads, n = kv->n_requests;
+  const int64_t row = at->n_q_heads * attn_part_floats(kv->head_dim) * (int64_t)sizeof(float);
+  int64_t rest = ((int64_t)n + decode_chunks(decode_units(n, kv->n_kv_heads, group))) * row;
+  if (bits == 4) {  // (enough for any window)
+    const Decode4 d = decode4_plan(n, kv->n_kv_heads, group, kv->head_dim, kv->max_blocks * kv->tokens_per_page, 0);
+    rest = std::max(rest, decode4_cut_bytes(n) + 2 * row * d.spans);
+  }
+  return kAttnCounterBytes + rest;
 }
 
 inline int64_t prefill_workspace(const slora_kv* kv, const slora_attn* at, int32_t n_tokens) {
@@ -148,12 +155,12 @@ inline int workspace_size(const char* what, int bits, const slora_kv* kv, const 
   if (n_tokens < 0) return fail(SLORA_E_INVALID, "%s: n_tokens %d < 0", what, n_tokens);
   const int rc = check_heads(what, bits, kv, at);
   if (rc) return rc;
-  *bytes = n_tokens ? prefill_workspace(kv, at, n_tokens) : decode_workspace(kv, at);
+  *bytes = n_tokens ? prefill_workspace(kv, at, n_tokens) : decode_workspace(bits, kv, at);
   return SLORA_OK;
 }
 
 // Checks an attention call and fills the kernels' arguments.
-inline int attn_args(const char* what, const slora_kv* kv, const slora_attn* at, void* ws, int64_t ws_bytes, int64_t need,
+inline int attn_args(const char* what, int bits, const slora_kv* kv, const slora_attn* at, void* ws, int64_t ws_bytes, int64_t need,
               AttnArgs* a) {
   if (!(at->softcap >= 0.f) || !std::isfinite(at->softcap) || !std::isfinite(at->scale))
     return fail(SLORA_E_INVALID, "%s: scale %g must be finite and softcap %g finite and >= 0", what, (double)at->scale,
@@ -208,7 +215,14 @@ inline int attn_args(const char* what, const slora_kv* kv, const slora_attn* at,
   a->part = (float*)((uint8_t*)ws + kAttnCounterBytes);
   a->wg_heads = decode_wg_heads(a->n_req, a->hk, a->group);
   a->chunks = decode_chunks(decode_units(a->n_req, a->hk, a->group));
-  a->kv4 = kv4_layout(a->hk, a->D);
+  if (bits == 4) {
+    const Decode4 d = decode4_plan(a->n_req, a->hk, a->group, a->D, a->max_len, a->window);
+    a->kv4 = kv4_layout(a->hk, a->D);
+    a->wave_heads = d.heads;
+    a->wave_runs = d.runs;
+    a->wg_units = d.wg_units;
+    a->spans = d.spans;
+  }
   return SLORA_OK;
 }
 
@@ -220,7 +234,11 @@ inline int attn_decode(const char* what, int bits, int id, LaunchAttn launch, co
   if (rc) return rc;
   if (kv->n_requests == 0) return SLORA_OK;
   AttnArgs a;
-  if ((rc = attn_args(what, kv, at, ws, ws_bytes, decode_workspace(kv, at), &a))) return rc;
+  if ((rc = attn_args(what, bits, kv, at, ws, ws_bytes, decode_workspace(bits, kv, at), &a))) return rc;
+  if (a.spans) {
+    a.cut = (int2*)a.part;
+    a.part += decode4_cut_bytes(a.n_req) / (int64_t)sizeof(float);
+  }
   const hipStream_t s = (hipStream_t)stream;
   const hipError_t e = timed_call(id, s, [&](const LaunchEvents& ev) { return launch(a, kv->dtype, s, ev); });
   return e == hipSuccess ? SLORA_OK : launch_failed(e, what);
@@ -236,7 +254,7 @@ inline int attn_prefill(const char* what, int bits, int id, LaunchAttn launch, c
   if (kv->n_requests == 0 || n_tokens == 0) return SLORA_OK;
   if (!q_offsets) return fail(SLORA_E_INVALID, "%s: q_offsets is NULL", what);
   AttnArgs a;
-  if ((rc = attn_args(what, kv, at, ws, ws_bytes, prefill_workspace(kv, at, n_tokens), &a))) return rc;
+  if ((rc = attn_args(what, bits, kv, at, ws, ws_bytes, prefill_workspace(kv, at, n_tokens), &a))) return rc;
   a.q_offsets = q_offsets;
   a.n_tok = n_tokens;
   a.chunks = prefill_chunks(n_tokens, a.group, a.hk, a.max_len);

@@ -640,7 +640,7 @@ int slora_attn_prefill(const slora_kv* kv, const slora_attn* attn, const int32_t
  * held by f16 and bf16 exactly, so slora_kv4_read gives what the attention calls see.
  *
  * Bytes of a token's K (or V): for every KV head its codes, 16 G bytes; then for every KV head
- * its G steps, a byte each, G rounded up to 1, 2, 4 or 8 bytes; the whole rounded up to 16. Codes
+ * its G steps, a byte each, filled up with zeros to 1, 2, 4 or 8 bytes; the whole rounded up to 16. Codes
  * of dimensions 32 c + 8 g .. + 7 are the 4 bytes from byte 4 (g G + c) of the head's on,
  * dimension 32 c + 8 g + e in bits 4 e of that word: the level's number, 8 added if negative. A
  * step's byte is the upper 8 of the 15 bits below the sign of its f16 value; 255: a NaN. (227 to

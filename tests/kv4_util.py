@@ -69,7 +69,7 @@ def token_bytes(code, step, sb):
     pair = code.view(n, hk, g, 4, 4, 2)
     byte = (pair[..., 0] | pair[..., 1] << 4).transpose(2, 3)  # [n, hk, 4, g, 4]
     out[:, :hk * 16 * g] = byte.reshape(n, -1)
-    steps = torch.full((n, hk, sb), -1, dtype=torch.int64)
+    steps = torch.zeros(n, hk, sb, dtype=torch.int64)
     steps[:, :, :g] = step
     out[:, hk * 16 * g:hk * (16 * g + sb)] = steps.view(n, -1)
     return out

@@ -116,6 +116,14 @@ DECODE = [
     ("f16", 1, 16, 160, 1, [70, 200], {}),
     ("bf16", 1, 17, 224, 1, [70, 200], {}),
     ("f16", 4, 8, 128, 16, [3000], {}),
+    ("f16", 40, 40, 128, 3, [90, 200, 1, 0, 33], {}),
+    ("bf16", 64, 64, 64, 2, [90, 130], {}),
+    ("f16", 15, 15, 96, 2, [70, 40], dict(slopes=True)),
+    ("bf16", 10, 30, 128, 4, [290, 65], {}),
+    ("f16", 6, 6, 200, 1, [150, 31], dict(cap=30.0)),
+    ("bf16", 30, 30, 192, 1, [45, 130], {}),
+    ("f16", 60, 60, 128, 1, [45, 130, 7], {}),
+    ("bf16", 3, 3, 128, 8, list(range(0, 140)), {}),
 ]
 
 
@@ -131,10 +139,20 @@ def options(kw, hq, n):
     return ref, own
 
 
+def long_table(hk, n, tpp):
+    """Blocks that make a table whose requests may have enough keys for the kernel of many keys."""
+    return -(-2600000 // (hk * n * tpp))
+
+
+@pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("dtype,hk,hq,d,tpp,lens,kw", DECODE)
-def test_decode(dtype, hk, hq, d, tpp, lens, kw):
+def test_decode(dtype, hk, hq, d, tpp, lens, kw, many):
     rng = np.random.default_rng(d + tpp)
-    c = four.Cache(rng, lens, dtype=dtype, hk=hk, d=d, tpp=tpp)
+    kw = dict(kw)
+    if many and kw.get("window"):
+        kw["window"] = 0  # (a window is few keys)
+    c = four.Cache(rng, lens, dtype=dtype, hk=hk, d=d, tpp=tpp,
+                   blocks_more=long_table(hk, len(lens), tpp) if many else 1)
     q = (torch.from_numpy(rng.standard_normal((len(lens), hq, d))) * 1.5).to(util.TORCH[dtype])
     ref_kw, own_kw = options(kw, hq, len(lens))
     scale = d ** -0.5
