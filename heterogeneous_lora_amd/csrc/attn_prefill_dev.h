@@ -249,36 +249,44 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
   // to LDS. A V that some row must not see is let in as zeros if it is no number.
   constexpr int kJobs = k4 ? KT : 1, kStepWords = NC <= 4 ? 1 : 2;
   const int quarter = tid & 3, my_key4 = (tid >> 2) & (BN - 1), job0 = KT == 2 ? 0 : tid >> 7;
-  uint32_t codes[kJobs][NC], steps[kJobs][kStepWords];
-  int32_t pages[kJobs];
+  struct Held {
+    uint32_t codes[kJobs][NC], steps[kJobs][kStepWords];
+  };
+  struct Pages {
+    int32_t id[kJobs];
+  };
+  Held held;
+  Pages pages;
   auto index4 = [&](int turn, int job) { return (turn + 2 - (job0 + job)) * BN + my_key4; };
   auto key4 = [&](int turn, int job) { return keys.key(max(min(index4(turn, job), keys.count - 1), 0)); };
   auto pages4 = [&](int turn) {
+    Pages x;
 #pragma unroll
     for (int j = 0; j < kJobs; ++j)
-      pages[j] = ((job0 + j ? a.vt : a.kt) + (int64_t)r * a.max_blocks)[div_tpp(a, (uint32_t)key4(turn, j))];
+      x.id[j] = ((job0 + j ? a.vt : a.kt) + (int64_t)r * a.max_blocks)[div_tpp(a, (uint32_t)key4(turn, j))];
+    return x;
   };
-  auto load4 = [&](int turn) {
+  auto load4 = [&](int turn, const Pages& pages, Held& to) {
 #pragma unroll
     for (int j = 0; j < kJobs; ++j) {
-      const Key4 k = key4_addr(a, pages[j], key4(turn, j), kv_head);
+      const Key4 k = key4_addr(a, pages.id[j], key4(turn, j), kv_head);
       const uint64_t at = k.good ? k.codes + quarter * 4 * a.kv4.groups : zeros;
       if (a.kv4.groups == NC) {
-        load_words<NC>(at, codes[j]);
+        load_words<NC>(at, to.codes[j]);
       } else {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) codes[j][c] = ((const SLORA_GLOBAL uint32_t*)at)[min(c, a.kv4.groups - 1)];
+        for (int c = 0; c < NC; ++c) to.codes[j][c] = ((const SLORA_GLOBAL uint32_t*)at)[min(c, a.kv4.groups - 1)];
       }
       const uint64_t st = index4(turn, j) >= keys.count ? zeros : k.good ? k.steps : (uint64_t)kAttnFill.nan_steps;
-      if (NC == 2 && a.kv4.groups == 1) load_steps<1>(st, steps[j]);
-      else load_steps<NC>(st, steps[j]);
+      if (NC == 2 && a.kv4.groups == 1) load_steps<1>(st, to.steps[j]);
+      else load_steps<NC>(st, to.steps[j]);
     }
   };
   // Unit u of a turn: job u / NC, group u % NC. edge: V's tile is one on some row's border.
-  auto put4 = [&](int turn, int u, bool edge) {
+  auto put4 = [&](int turn, int u, bool edge, const Held& from) {
     const int j = u / NC, c = u % NC;
     const bool v = job0 + j;
-    uint32_t st = steps[j][c >> 2], w = codes[j][c];
+    uint32_t st = from.steps[j][c >> 2], w = from.codes[j][c];
     if (NC != a.kv4.groups && c >= a.kv4.groups) st = w = 0;
     if (edge && v && (st >> c % 4 * 8 & 255) > kMaxStep) {
       sm_flag[0] = 1;
@@ -289,9 +297,9 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
                         : sm_k[turn & 1] + my_key4 * CH + (unit ^ S::k_swap(my_key4));
     *to = values8(w, step_twice(st, c & 3));
   };
-  auto put4_all = [&](int turn, int from, int to, bool edge) {
+  auto put4_all = [&](int turn, int units, bool edge, const Held& from) {
 #pragma unroll
-    for (int u = from; u < to; ++u) put4(turn, u, edge);
+    for (int u = 0; u < units; ++u) put4(turn, u, edge, from);
   };
   // Every row from position p0 to p1 sees every key of tile t.
   auto all_seen = [&](int t, int p0, int p1) {
@@ -305,16 +313,17 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
   int32_t next = 0;
   if (k4 && first_tile < n_tiles) {
     const int t = first_tile;
-    pages4(t - 2);
-    load4(t - 2);
+    // (all page ids, then all codes: two latencies)
+    const Pages p0 = pages4(t - 2), p1 = pages4(t - 1);
+    pages = pages4(t);
+    Held h0, h1;
+    load4(t - 2, p0, h0);
+    load4(t - 1, p1, h1);
+    load4(t, pages, held);
+    pages = pages4(t + 1);
     __syncthreads();  // sm_flag
-    if (job0 == 0) put4_all(t - 2, 0, NC, false);
-    pages4(t - 1);
-    load4(t - 1);
-    pages4(t);
-    put4_all(t - 1, 0, kJobs * NC, !all_seen(t, wg_p0, wg_p1));
-    load4(t);
-    pages4(t + 1);
+    if (job0 == 0) put4_all(t - 2, NC, false, h0);
+    put4_all(t - 1, kJobs * NC, !all_seen(t, wg_p0, wg_p1), h1);
     __syncthreads();
   }
   if (!k4 && first_tile < n_tiles) {  // turn t - 2 brings K of tile t, turn t - 1 V of tile t and K of tile t + 1
@@ -468,9 +477,9 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
       __syncthreads();
     }
     if (k4 && t >= w_tiles) {
-      put4_all(t, 0, kJobs * NC, !all_seen(t + 1, wg_p0, wg_p1));
-      load4(t + 1);
-      pages4(t + 2);
+      put4_all(t, kJobs * NC, !all_seen(t + 1, wg_p0, wg_p1), held);
+      load4(t + 1, pages, held);
+      pages = pages4(t + 2);
       continue;
     }
     if (t >= w_tiles) {
@@ -535,10 +544,10 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
     for (int i = 0; i < kSteps; ++i) {
       if (i + kAhead < kSteps) vfrag[i + kAhead] = v_frag(v_place, i + kAhead);
       if constexpr (k4) {
-        if (i % 2 == 0) put4(t, i / 2, edge_next);
+        if (i % 2 == 0) put4(t, i / 2, edge_next, held);
         if (i == kSteps - 1) {
-          load4(t + 1);
-          pages4(t + 2);
+          load4(t + 1, pages, held);
+          pages = pages4(t + 2);
         }
       } else {
         if (i == kSteps / 2) put_addr(t + 1, next);

@@ -313,6 +313,7 @@ struct AttnArgs {
   int32_t wg_units;         // waves of a workgroup on different heads
   int32_t spans;            // into which all requests' keys are cut
   int2* cut;                // [n_req]: the span a request begins in, the spans it is in
+  int32_t* back;            // prefill of 4 bits: tables and K and V in 16 bits, NULL: straight from the codes
   int32_t xcd_log2;         // 3 where spans go round the XCDs, else 0
 };
 // Floats of one row's partial result: max, sum, and the head's dimensions.
@@ -377,6 +378,26 @@ inline int32_t attn_instance(int32_t D) {
 inline int32_t prefill_chunks(int64_t n_tok, int32_t group, int32_t hk, int32_t max_len) {
   const int64_t tiles = (n_tok * group + 127) / 128;
   return max_len <= 512 || tiles * hk >= 2 * kDecodeTarget ? 0 : (kDecodeTarget + hk - 1) / hk;
+}
+// Prefill of 4 bits: whether keys are read back to 16 bits first, where each would otherwise be made
+// values of by 32 row tiles and more (64 of heads of 256); blocks of a request then, bytes of the two
+// tables and of K and V. us straight from the codes and read back, 32 query heads on 8 of 128: 1024
+// tokens of 16 requests (4096 rows) 286 and 258, after 16000 cached 357 and 321; 512 of 8 (2048) 61 and
+// 67, 256 after 8192 (1024) 77 and 89; heads of 256 at 4096 rows 189 and 211.
+struct Prefill4 {
+  bool back;
+  int32_t blocks;
+  int64_t table_bytes, bytes;
+};
+constexpr int32_t kBackTokens = 64;                    // of a block
+constexpr int64_t kBackBytes = int64_t(1) << 30;       // at most
+inline Prefill4 prefill4_plan(int32_t n_req, int64_t n_tok, int32_t group, int32_t hk, int32_t D, int32_t max_len) {
+  Prefill4 p;
+  p.blocks = (max_len + kBackTokens - 1) / kBackTokens;
+  p.table_bytes = ((int64_t)n_req * p.blocks * 8 + 255) / 256 * 256;
+  p.bytes = (int64_t)n_req * p.blocks * kBackTokens * hk * D * 4;
+  p.back = n_tok * group >= (int64_t)n_req * (D > 128 ? 32 * D : 4096) && p.bytes > 0 && p.bytes <= kBackBytes;
+  return p;
 }
 inline int32_t prefill_waves(int64_t n_tok, int32_t group) {
   return n_tok * group >= 128 ? 4 : (int32_t)((n_tok * group + 31) / 32);

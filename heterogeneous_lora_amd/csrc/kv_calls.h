@@ -147,6 +147,15 @@ inline int64_t prefill_workspace(const slora_kv* kv, const slora_attn* at, int32
   return kAttnCounterBytes + 2 * chunks * kv->n_kv_heads * prefill_waves(n_tokens, group) *
                                  part_floats(attn_instance(kv->head_dim)) * (int64_t)sizeof(float);
 }
+inline Prefill4 prefill4_of(const slora_kv* kv, const slora_attn* at, int32_t n_tokens) {
+  return prefill4_plan(kv->n_requests, n_tokens, at->n_q_heads / kv->n_kv_heads, kv->n_kv_heads, kv->head_dim,
+                       kv->max_blocks * kv->tokens_per_page);
+}
+inline int64_t prefill_workspace(int bits, const slora_kv* kv, const slora_attn* at, int32_t n_tokens) {
+  const int64_t rest = prefill_workspace(kv, at, n_tokens);
+  const Prefill4 p = prefill4_of(kv, at, n_tokens);
+  return bits == 4 && p.back ? (rest + 255) / 256 * 256 + p.table_bytes + p.bytes : rest;
+}
 
 inline int workspace_size(const char* what, int bits, const slora_kv* kv, const slora_attn* at, int32_t n_tokens,
                    int64_t* bytes) {
@@ -155,7 +164,7 @@ inline int workspace_size(const char* what, int bits, const slora_kv* kv, const 
   if (n_tokens < 0) return fail(SLORA_E_INVALID, "%s: n_tokens %d < 0", what, n_tokens);
   const int rc = check_heads(what, bits, kv, at);
   if (rc) return rc;
-  *bytes = n_tokens ? prefill_workspace(kv, at, n_tokens) : decode_workspace(bits, kv, at);
+  *bytes = n_tokens ? prefill_workspace(bits, kv, at, n_tokens) : decode_workspace(bits, kv, at);
   return SLORA_OK;
 }
 
@@ -254,11 +263,13 @@ inline int attn_prefill(const char* what, int bits, int id, LaunchAttn launch, c
   if (kv->n_requests == 0 || n_tokens == 0) return SLORA_OK;
   if (!q_offsets) return fail(SLORA_E_INVALID, "%s: q_offsets is NULL", what);
   AttnArgs a;
-  if ((rc = attn_args(what, bits, kv, at, ws, ws_bytes, prefill_workspace(kv, at, n_tokens), &a))) return rc;
+  if ((rc = attn_args(what, bits, kv, at, ws, ws_bytes, prefill_workspace(bits, kv, at, n_tokens), &a))) return rc;
   a.q_offsets = q_offsets;
   a.n_tok = n_tokens;
   a.chunks = prefill_chunks(n_tokens, a.group, a.hk, a.max_len);
   a.part_waves = prefill_waves(n_tokens, a.group);
+  if (bits == 4 && prefill4_of(kv, at, n_tokens).back)
+    a.back = (int32_t*)((uint8_t*)ws + (prefill_workspace(kv, at, n_tokens) + 255) / 256 * 256);
   const hipStream_t s = (hipStream_t)stream;
   const hipError_t e = timed_call(id, s, [&](const LaunchEvents& ev) { return launch(a, kv->dtype, s, ev); });
   return e == hipSuccess ? SLORA_OK : launch_failed(e, what);

@@ -6,7 +6,7 @@ arithmetic. u = finfo(storage type).eps / 2 is one rounding of the result. A row
   (weight + 2 d + 2^-18) sum_j w_j |v_j|  +  floor sum_j |v_j|  +  u |out|
 weight, floor: what a weight loses on its way to the product with V, which takes f16 whatever the
 storage type: 2^-11 of it and 2^-32 of the largest where it is rounded once, 2^-21 and 2^-31 where
-it goes in as two values (slora_attn4_decode with f16 q). d: the error of a score: 2^-24 (D + 16)
+it goes in as two values (slora_attn4_decode with f16 q); long prompts with bf16 q round it to bf16. d: the error of a score: 2^-24 (D + 16)
 max_j scale sum |q||k_j| for the products in any order and their scaling, 2^-22 max_j |s_j| for
 the roundings behind them, with a softcap 2^-22 of it up to 256 and 2^-19 max_j |s_j| above.
 2^-18: sums over keys in 32 bits."""
@@ -160,7 +160,10 @@ def attention(c, q, rows, *, scale, cap=0.0, window=0, slopes=None, prefix=None,
     return SimpleNamespace(out=out, mass=mass, total=total, d=d, lse=lse)
 
 
-def bound(ref, dtype, decode):
+def bound(ref, dtype, decode, back=False):
+    """back: keys were read back to the storage type first (long prompts), weights are then of it."""
     u, tiny = half_step(dtype)
     weight, floor = (2.0 ** -21, 2.0 ** -31) if decode and dtype == "f16" else (2.0 ** -11, 2.0 ** -32)
+    if back and dtype == "bf16":
+        weight, floor = u, 0.0
     return (weight + 2 * ref.d + 2.0 ** -18) * ref.mass + floor * ref.total + u * ref.out.abs() + tiny
