@@ -7,11 +7,15 @@
 // magnitude is that of its pieces, which travel between the lanes of a head through LDS.
 //
 // A code is a decision: two ways of rounding K that differ in the last of 32 bits would now and
-// then pick another level, a sixth of the group's range away. So K's norm, rotation, step and
-// quotient are in 64 bits, which the vector unit does at the rate of 32, and x / step is
-// corrected and cut to a float in a way that no border is met or passed: the level is that of the
-// exactly computed value, unless 2^-50 of it decides. (V has no arithmetic before its
-// step, and is exact.)
+// then pick another level, a sixth of the group's range away. So K's norm and rotation are in 64
+// bits. What comes after needs only to know on which side of few-bit numbers a value lies (levels'
+// borders times the step, ties of the step times 6), which its 24 leading bits say if the last one
+// is set where something is cut off: step and level are those of the exactly computed value, unless
+// 2^-50 of it decides. (V has no arithmetic before its step, and is exact.)
+//
+// Bound by the vector unit (65% of its cycles while it has work), which K keeps busy longest. 16411
+// tokens of 32 query and 8 + 8 KV heads of 128 with norms: 127 us (131 with the steps and quotients in 64 bits too;
+// slora_kv_write, whose pool is four times as large: 91).
 #include "kv_write_dev.h"
 
 namespace slora {
@@ -22,46 +26,42 @@ struct Write4 {
   Kv4Layout lay;
 };
 
+// x cut off to 24 bits, the last of them set if anything was lost (a multiple of 2^-149; an infinity
+// from 2^128 on).
+__device__ __forceinline__ float cut(double x) {
+  const float f = (float)x;
+  const double lost = fabs(x) - fabs((double)f);
+  const int bits = __float_as_int(f);
+  return __int_as_float(lost == 0.0 || !(fabsf(f) < INFINITY) ? bits : (lost < 0.0 ? bits - 1 : bits) | 1);
+}
+
 // Upper bits of the f16 value nearest to `most` / 6 among those with 3 bits behind the leading
 // one: a group's step byte. 226 is the largest whose 6-fold is finite in f16.
 constexpr int kMaxStep = 226, kNanStep = 255;
-__device__ __forceinline__ int step_byte(double most) {
+__device__ __forceinline__ int step_byte(float most) {
   if (!(most < INFINITY)) return kNanStep;
-  const double x = most / 6.0;
+  const float x = most / 6.0f;
   // multiples of 2^(e - 3), e = the exponent, -14 at least
-  const int e = max((int)((__double2hiint(x) >> 20) & 0x7ff) - 1023, -14);
+  const int e = max((__float_as_int(x) >> 23) - 127, -14);
   if (e > 14) return kMaxStep;
-  const int n = (int)rint(ldexp(x, 3 - e));  // 0 .. 16
-  return min((e + 14) * 8 + n, kMaxStep);    // n = 16 carries into the exponent
-}
-__device__ __forceinline__ float step_value(int byte) {
-  return (float)__builtin_bit_cast(_Float16, (uint16_t)(byte << 7));
+  const int n = (int)rintf(ldexpf(x, 3 - e));  // 0 .. 16
+  return min((e + 14) * 8 + n, kMaxStep);      // n = 16 carries into the exponent
 }
 
-// x / step, as a float on the same side of every level's border: cut off towards zero and made
-// odd if anything was lost (the borders have few bits, so no odd float is one).
-__device__ __forceinline__ float quotient(double x, double step, double inv) {
-  double t = x * inv;
-  t = fma(fma(-t, step, x), inv, t);
-  const float f = (float)t;
-  const double lost = fabs(t) - fabs((double)f);
-  const int bits = __float_as_int(f);
-  return __int_as_float(lost == 0.0 ? bits : (lost < 0.0 ? bits - 1 : bits) | 1);
-}
-__device__ __forceinline__ float quotient(float x, float step, float inv) {
-  const float t = x * inv;
-  return fmaf(fmaf(-t, step, x), inv, t);
-}
-
-// Codes of a piece, 4 bits each.
-template <int V, typename F>
-__device__ __forceinline__ uint32_t codes_of(const F (&x)[V], int byte) {
-  const float step = byte < kNanStep ? step_value(byte) : 0.f;
-  const F s = (F)step, inv = step == 0.f ? (F)0 : (F)1 / s;
-  uint32_t w = 0;
+// Codes of a piece, 4 bits each. The quotient is the nearest float to x / step: corrected, as the
+// product with a rounded reciprocal may pass a border.
+template <int V>
+__device__ __forceinline__ uint32_t codes_of(const float (&x)[V], int byte) {
+  const float step = byte < kNanStep ? (float)__builtin_bit_cast(_Float16, (uint16_t)(byte << 7)) : 0.f;
+  const float inv = step == 0.f ? 0.f : 1.0f / step;
   float t[V];
 #pragma unroll
-  for (int e = 0; e < V; ++e) t[e] = fminf(fmaxf(step == 0.f ? 0.f : quotient(x[e], s, inv), -6.f), 6.f);
+  for (int e = 0; e < V; ++e) {
+    t[e] = x[e] * inv;
+    t[e] = fmaf(fmaf(-t[e], step, x[e]), inv, t[e]);
+    t[e] = step == 0.f ? 0.f : fminf(fmaxf(t[e], -6.f), 6.f);
+  }
+  uint32_t w = 0;
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[0], t[1], 1.0f, 0);
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[2], t[3], 1.0f, 1);
   if constexpr (V == 8) {
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(Write4 b) {
   const WriteArgs& a = b.a;
   const Kv4Layout& lay = b.lay;
   __shared__ double2 angle[kAngles];
-  __shared__ double sm_most[kThreads * 2];  // largest magnitudes of the pieces, by group of lanes
+  __shared__ uint32_t sm_most[kThreads * 2];  // largest magnitudes of the pieces, by group of lanes
   const int tid = (int)threadIdx.x;
   const int tok0 = (int)blockIdx.x * a.tpw, n_tok = min(a.tpw, a.n_tok - tok0);
   const int pairs = a.pairs;
@@ -92,20 +92,16 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(Write4 b) {
   __syncthreads();
 
   const Place at = place_of<V, INTER>(a, tid % G);
-  double* const most = sm_most + tid / G * 2 * G;
+  uint32_t* const most = sm_most + tid / G * 2 * G;
 
-  // What the cache holds of the lane's pieces x and y, to the head at `dst`.
-  auto put = [&](uint8_t* token, int hh, const auto& x, const auto& y) {
-    double mx = 0.0, my = 0.0;
+  // What the cache holds of the lane's pieces x and y, to head hh of a token. (Magnitudes are
+  // compared as whole numbers, in which an infinity is above all others and NaN above that.)
+  auto put = [&](uint8_t* token, int hh, const float (&x)[V], const float (&y)[V]) {
+    uint32_t mx = 0, my = 0;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      mx = fmax(mx, fabs((double)x[e]));  // (passes over NaN)
-      my = fmax(my, fabs((double)y[e]));
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      if (x[e] != x[e]) mx = INFINITY;
-      if (y[e] != y[e]) my = INFINITY;
+      mx = max(mx, __float_as_uint(x[e]) & 0x7fffffffu);
+      my = max(my, __float_as_uint(y[e]) & 0x7fffffffu);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     most[at.c0] = mx;
@@ -113,16 +109,16 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(Write4 b) {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     constexpr int kIn = 32 / V;  // pieces of a group of 32
-    auto store = [&](int c, const auto& z) {
+    auto store = [&](int c, const float (&z)[V]) {
       const int group = c / kIn;
       if (group >= lay.groups) {  // a head's steps are filled up with zeros
         if (c % kIn == 0 && group < lay.step_bytes) token[lay.steps_at + hh * lay.step_bytes + group] = 0;
         return;
       }
-      double m = 0.0;
+      uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < kIn; ++i) m = fmax(m, most[group * kIn + i]);
-      const int byte = step_byte(m);
+      for (int i = 0; i < kIn; ++i) m = max(m, most[group * kIn + i]);
+      const int byte = step_byte(__uint_as_float(m));
       const uint32_t w = codes_of<V>(z, byte);
       const int p = c * V / 8, word = (p & 3) * lay.groups + (p >> 2);  // its 8 dimensions' place
       uint8_t* to = token + hh * 16 * lay.groups + word * 4;
@@ -175,7 +171,12 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(Write4 b) {
         ky[e] = y[e];
       }
       norm_and_turn<DT, V, G, INTER>(a, ang, a.kw, at, kx, ky);
-      put(token, hh, kx, ky);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        x[e] = cut(kx[e]);
+        y[e] = cut(ky[e]);
+      }
+      put(token, hh, x, y);
     }
   }
 }
