@@ -1,8 +1,9 @@
 // K and V of tokens out of a cache in 4 bits (slora_kv4_read): value = step * level, which both
 // storage types hold exactly.
 //
-// Bound by the bytes written: 16 for each 4 of codes read. A thread takes 8 dimensions, so that a
-// wave's stores are whole lines.
+// Bound by the bytes written: 16 for each 4 of codes read. A thread takes 4 pieces of 8 dimensions,
+// each wave's pieces neighbours, so that its stores are whole lines. K and V of 65000 tokens of 8
+// heads of 128: 70 us (4.8 TB/s, as a copy; 94 us where each piece waited for its own slot).
 #include "device_common.h"
 #include "kv4_calls.h"
 
@@ -33,28 +34,44 @@ __global__ __launch_bounds__(kThreads) void kv4_read_kernel(ReadArgs a) {
   if (!a.out[which]) return;
   const int64_t first = (int64_t)blockIdx.x * (kUnits * kThreads), tok0 = first / a.per_token;
   const uint32_t in0 = (uint32_t)(first - tok0 * a.per_token) + threadIdx.x;
+  // (the units' slots together, then their codes: no wait for memory stands between two of them)
+  uint32_t t[kUnits], in[kUnits];
+  int64_t slot[kUnits];
 #pragma unroll
   for (int k = 0; k < kUnits; ++k) {
-    const uint32_t t = divided(in0 + k * kThreads, a.per_token, a.token_magic, a.token_shift);
-    const int64_t tok = tok0 + t;
-    if (tok >= a.n_tok) return;
-    const uint32_t in = in0 + k * kThreads - t * a.per_token;
-    const uint32_t head = divided(in, a.per_head, a.head_magic, a.head_shift), p = in - head * a.per_head;
-    const int64_t slot = a.slots[which][tok];
-    const int64_t page = (slot >> 31) ? slot / a.tpp : (int64_t)divided((uint32_t)slot, a.tpp, a.tpp_magic, a.tpp_shift);
-    if (slot < 0 || page >= a.n_pages) continue;
-    const uint8_t* token = a.pool + page * a.page_bytes + (slot - page * a.tpp) * a.lay.token_bytes;
-    const uint32_t w =
-        *reinterpret_cast<const uint32_t*>(token + (head * 4 * a.lay.groups + (p & 3) * a.lay.groups + (p >> 2)) * 4);
-    const uint32_t byte = token[a.lay.steps_at + head * a.lay.step_bytes + (p >> 2)];
-    const float step = (float)__builtin_bit_cast(_Float16, (uint16_t)(byte << 7));
+    t[k] = divided(in0 + k * kThreads, a.per_token, a.token_magic, a.token_shift);
+    in[k] = in0 + k * kThreads - t[k] * a.per_token;
+    slot[k] = a.slots[which][min(tok0 + t[k], (int64_t)a.n_tok - 1)];
+  }
+  uint32_t w[kUnits], byte[kUnits], head[kUnits], piece[kUnits];
+  bool is[kUnits];
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    head[k] = divided(in[k], a.per_head, a.head_magic, a.head_shift);
+    piece[k] = in[k] - head[k] * a.per_head;
+    const int64_t at = slot[k],
+                  page = (at >> 31) ? at / a.tpp : (int64_t)divided((uint32_t)at, a.tpp, a.tpp_magic, a.tpp_shift);
+    is[k] = tok0 + t[k] < a.n_tok && at >= 0 && page < a.n_pages;
+    const uint8_t* token = a.pool + page * a.page_bytes + (at - page * a.tpp) * a.lay.token_bytes;
+    const uint32_t group = piece[k] >> 2, word = head[k] * 4 * a.lay.groups + (piece[k] & 3) * a.lay.groups + group;
+    const uint8_t* const zero = reinterpret_cast<const uint8_t*>(dev::fill_zero());
+    const uint8_t* const codes = is[k] ? token + word * 4 : zero;
+    const uint8_t* const step = is[k] ? token + a.lay.steps_at + head[k] * a.lay.step_bytes + group : zero;
+    w[k] = *(const __attribute__((address_space(1))) uint32_t*)codes;
+    byte[k] = *(const __attribute__((address_space(1))) uint8_t*)step;
+  }
+#pragma unroll
+  for (int k = 0; k < kUnits; ++k) {
+    if (!is[k]) continue;
+    const float step = (float)__builtin_bit_cast(_Float16, (uint16_t)(byte[k] << 7));
     uint32_t o[4];
     auto two = [&](auto x, int i) { o[i] = dev::pack2<DT>((float)x[0] * step, (float)x[1] * step); };
-    two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), 0);
-    two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1), 1);
-    two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), 2);
-    two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3), 3);
-    dev::st16(a.out[which] + tok * a.ts[which] + (int64_t)head * a.hs[which] + p * 8, make_uint4(o[0], o[1], o[2], o[3]));
+    two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[k], 1.0f, 0), 0);
+    two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[k], 1.0f, 1), 1);
+    two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[k], 1.0f, 2), 2);
+    two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[k], 1.0f, 3), 3);
+    dev::st16(a.out[which] + (tok0 + t[k]) * a.ts[which] + (int64_t)head[k] * a.hs[which] + piece[k] * 8,
+              make_uint4(o[0], o[1], o[2], o[3]));
   }
 }
 
