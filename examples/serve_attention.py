@@ -28,6 +28,7 @@ def main():
     p.add_argument("--requests", type=int, default=24)
     p.add_argument("--window", type=int, default=0, help="sliding window, 0: none")
     p.add_argument("--softcap", type=float, default=0.0)
+    p.add_argument("--kv-bits", type=int, default=16, choices=(16, 4), help="of a cached value")
     p.add_argument("--seed", type=int, default=0)
     args = p.parse_args()
     heads, kv_heads, dim = 16, 4, 64
@@ -36,7 +37,7 @@ def main():
                                 rank_choices=(8, 16, 32, 64))
     loop = runtime.AttentionLoop(wl, n_pages=20000, n_q_heads=heads, n_kv_heads=kv_heads, head_dim=dim, max_len=256,
                                  rope=runtime.Rope(dim), attention=dict(window=args.window, softcap=args.softcap),
-                                 max_batch_tokens=1024, max_running=64)
+                                 max_batch_tokens=1024, max_running=64, kv_bits=args.kv_bits)
     rng = np.random.default_rng(args.seed)
     for r in range(args.requests):
         loop.submit(r, int(rng.integers(wl.n_adapters)), int(rng.integers(8, 160)), int(rng.integers(4, 32)))

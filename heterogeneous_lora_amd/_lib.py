@@ -173,6 +173,7 @@ def load(path: str = LIB_PATH):
         "slora_residency_info": ([P, P], I),
         "slora_residency_is_resident": ([P, I, P], I),
         "slora_sched_create": ([P, P, P, P], I),
+        "slora_sched_create_paged": ([P, P, P, I, P], I),
         "slora_sched_destroy": ([P], I),
         "slora_sched_submit": ([P, _c_i64, I, I, I, I, _c_i64], I),
         "slora_sched_finish": ([P, _c_i64], I),
@@ -377,16 +378,18 @@ def _arr(ptr, n, dtype):
 
 
 class Scheduler:
-    """slora_sched: FIFO continuous-batching admission over the unified pool."""
+    """slora_sched: FIFO continuous-batching admission over the unified pool. A page holds
+    tokens_per_page tokens of a request."""
 
     def __init__(self, pool: Pool, residency: Optional[Residency], kv_pages_per_token: int,
-                 max_batch_tokens: int, max_running: int):
+                 max_batch_tokens: int, max_running: int, tokens_per_page: int = 1):
         self._lib = load()
         self.pool, self.residency = pool, residency
         cfg = SchedConfig(kv_pages_per_token, max_batch_tokens, max_running)
         h = ctypes.c_void_p()
-        _check(self._lib.slora_sched_create(pool.handle, residency.handle if residency else None,
-                                            ctypes.byref(cfg), ctypes.byref(h)), "sched_create")
+        _check(self._lib.slora_sched_create_paged(pool.handle, residency.handle if residency else None,
+                                                  ctypes.byref(cfg), tokens_per_page, ctypes.byref(h)),
+               "sched_create")
         self.handle = h
 
     def destroy(self):

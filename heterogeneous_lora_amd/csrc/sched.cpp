@@ -27,9 +27,10 @@
 // most recently admitted requests are aborted until the rest fit.
 //
 // KV pages: one page holds one token's K or V vector for one layer (page = hidden
-// size), so a token takes kv_pages_per_token pages. Every batch a step produces is a
-// slora_routing: the prompts of newly admitted requests as segments, then one decode
-// token per running request.
+// size), so a token takes kv_pages_per_token pages; where a page holds more tokens' (fewer
+// heads, or a cache in 4 bits) as many tokens of a request share a set of pages. Every batch a
+// step produces is a slora_routing: the prompts of newly admitted requests as segments, then
+// one decode token per running request.
 #include <string.h>
 
 #include <algorithm>
@@ -171,7 +172,10 @@ struct slora_sched {
     int32_t adapter = -1, rank = 0, prompt = 0, max_new = 0, generated = 0;
     int64_t deadline = -1;
     std::vector<int32_t> kv;  // KV pages held
+    // Tokens whose K and V are cached: the prompt, and all but the last of the new ones.
+    int64_t cached() const { return (int64_t)prompt + generated - 1; }
   };
+  int32_t tokens_per_page = 1;
   std::deque<Req> queue;
   std::vector<Req> running;  // in admission order
   std::set<int64_t> ids;     // ids waiting or running
@@ -254,9 +258,15 @@ int do_step(slora_sched* s) {
     }
   }
 
-  // 2. every running request decodes one token, which needs ppt more KV pages; the most
-  //    recently admitted requests are aborted while the pool cannot hold them all
-  while (!s->running.empty() && pool_free(s->pool) < (int64_t)s->running.size() * ppt) {
+  // 2. every running request decodes one token, which needs ppt more KV pages where those it
+  //    has are full; the most recently admitted requests are aborted while the pool cannot
+  //    hold them all
+  const int64_t tpp = s->tokens_per_page;
+  auto full = [&](const slora_sched::Req& q) { return q.cached() % tpp == 0; };
+  int64_t decode_need = 0;
+  for (const auto& q : s->running) decode_need += full(q) ? ppt : 0;
+  while (!s->running.empty() && pool_free(s->pool) < decode_need) {
+    decode_need -= full(s->running.back()) ? ppt : 0;
     rc = retire(s, s->running.back());
     if (rc) return rc;
     note_abort(s, s->running.back().id, SLORA_ABORT_POOL_FULL);
@@ -264,10 +274,12 @@ int do_step(slora_sched* s) {
   }
   int64_t tokens = 0;
   for (auto& q : s->running) {
-    const size_t at = q.kv.size();
-    q.kv.resize(at + (size_t)ppt);
-    rc = slora_pool_alloc_kv(s->pool, ppt, q.kv.data() + at);
-    if (rc) return rc;  // cannot happen: the pages were counted above
+    if (full(q)) {
+      const size_t at = q.kv.size();
+      q.kv.resize(at + (size_t)ppt);
+      rc = slora_pool_alloc_kv(s->pool, ppt, q.kv.data() + at);
+      if (rc) return rc;  // cannot happen: the pages were counted above
+    }
     s->token_adapter.push_back(q.adapter);
     s->token_request.push_back(q.id);
     ++q.generated;
@@ -282,7 +294,7 @@ int do_step(slora_sched* s) {
   while (!s->queue.empty() && (int64_t)s->running.size() + (int64_t)admitted.size() < s->cfg.max_running) {
     slora_sched::Req& q = s->queue.front();
     if (tokens + q.prompt > s->cfg.max_batch_tokens) break;
-    const int64_t kv_need = (int64_t)q.prompt * ppt;
+    const int64_t kv_need = (q.prompt + tpp - 1) / tpp * ppt;
     const bool lora = s->res && q.adapter >= 0 && q.rank > 0;
     if (lora) {
       // room for the adapter (unless resident) and the prompt's KV together, from free
@@ -324,6 +336,26 @@ int do_step(slora_sched* s) {
   }
   // the batch: the new prompts (segments) first, then the decode tokens
   for (auto& q : admitted) s->running.push_back(std::move(q));
+  return SLORA_OK;
+}
+
+int create(slora_pool* pool, slora_residency* res, const slora_sched_config* cfg, int32_t tokens_per_page,
+           slora_sched** out) {
+  clear_error();
+  if (!out) return fail(SLORA_E_INVALID, "sched_create: out is NULL");
+  *out = nullptr;
+  if (!pool || !cfg) return fail(SLORA_E_INVALID, "sched_create: pool / config is NULL");
+  if (cfg->kv_pages_per_token < 1 || cfg->max_running < 1 || cfg->max_batch_tokens < cfg->max_running)
+    return fail(SLORA_E_INVALID, "sched_create: kv_pages_per_token, max_running >= 1 and "
+                "max_batch_tokens >= max_running required");
+  if (tokens_per_page < 1) return fail(SLORA_E_INVALID, "sched_create: tokens_per_page %d", tokens_per_page);
+  auto* s = new slora_sched;
+  s->pool = pool;
+  s->res = res;
+  s->cfg = *cfg;
+  s->tokens_per_page = tokens_per_page;
+  s->seg_offsets.assign(1, 0);
+  *out = s;
   return SLORA_OK;
 }
 
@@ -423,22 +455,12 @@ int slora_residency_is_resident(const slora_residency* r, int32_t adapter_id, in
 
 int slora_sched_create(slora_pool* pool, slora_residency* res, const slora_sched_config* cfg,
                        slora_sched** out) {
-  return guarded(__func__, [&] {
-    clear_error();
-    if (!out) return fail(SLORA_E_INVALID, "sched_create: out is NULL");
-    *out = nullptr;
-    if (!pool || !cfg) return fail(SLORA_E_INVALID, "sched_create: pool / config is NULL");
-    if (cfg->kv_pages_per_token < 1 || cfg->max_running < 1 || cfg->max_batch_tokens < cfg->max_running)
-      return fail(SLORA_E_INVALID, "sched_create: kv_pages_per_token, max_running >= 1 and "
-                  "max_batch_tokens >= max_running required");
-    auto* s = new slora_sched;
-    s->pool = pool;
-    s->res = res;
-    s->cfg = *cfg;
-    s->seg_offsets.assign(1, 0);
-    *out = s;
-    return SLORA_OK;
-  });
+  return guarded(__func__, [&] { return create(pool, res, cfg, 1, out); });
+}
+
+int slora_sched_create_paged(slora_pool* pool, slora_residency* res, const slora_sched_config* cfg,
+                             int32_t tokens_per_page, slora_sched** out) {
+  return guarded(__func__, [&] { return create(pool, res, cfg, tokens_per_page, out); });
 }
 
 int slora_sched_destroy(slora_sched* s) {

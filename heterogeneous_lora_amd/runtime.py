@@ -208,7 +208,8 @@ class ServingLoop:
     data (the same generators the tests and the oracle use)."""
 
     def __init__(self, wl, n_pages: int, kv_pages_per_token: int = 2, max_batch_tokens: int = 4096,
-                 max_running: int = 512, proj: int = 0, device: str = "cuda", seed: int = 0):
+                 max_running: int = 512, proj: int = 0, device: str = "cuda", seed: int = 0,
+                 tokens_per_page: int = 1):
         self.wl, self.proj, self.device = wl, proj, torch.device(device)
         p = wl.projections[proj]
         self.d_in, self.d_out = p.d_in, p.d_out
@@ -219,7 +220,7 @@ class ServingLoop:
         self.pool = _lib.Pool(self.pool_t.data_ptr(), n_pages, P, wl.dtype, seed)
         self.res = _lib.Residency(self.pool, [p.d_in], [p.d_out])
         self.sched = _lib.Scheduler(self.pool, self.res, kv_pages_per_token, max_batch_tokens,
-                                    max_running)
+                                    max_running, tokens_per_page)
         # the projection alone (its weights are drawn as projection 0 of this workload)
         self.one = dataclass_replace(wl, projections=[p], _cache={})
         self.store = HostStore(self.one, list(range(wl.n_adapters)))
@@ -545,16 +546,25 @@ class AttentionLoop(ServingLoop):
 
     d_out of the projection is (n_q_heads + 2 n_kv_heads) * head_dim; max_len bounds a
     request's cached tokens. attention: softcap, window, slopes, scale as KVCache.bind_decode takes
-    them; write: norm, q_weight, k_weight, eps as KVCache.bind_write does."""
+    them; write: norm, q_weight, k_weight, eps as KVCache.bind_write does. kv_bits: of a cached
+    value, 16 or 4; a K page and a V page hold tokens_per_page tokens (None: one in 16 bits, as
+    many as fit in 4)."""
 
     def __init__(self, wl, n_pages: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_len: int,
-                 rope: Optional[Rope] = None, attention: Optional[dict] = None, write: Optional[dict] = None, **kw):
-        super().__init__(wl, n_pages, kv_pages_per_token=2, **kw)  # a K page and a V page a token
+                 rope: Optional[Rope] = None, attention: Optional[dict] = None, write: Optional[dict] = None,
+                 kv_bits: int = 16, tokens_per_page: Optional[int] = None, **kw):
+        if tokens_per_page is None:
+            tokens_per_page = 1
+            if kv_bits == 4:
+                tokens_per_page = max(2 * wl.page_elems // _lib.kv4_token_bytes(n_kv_heads, head_dim), 1)
+        super().__init__(wl, n_pages, kv_pages_per_token=2, tokens_per_page=tokens_per_page, **kw)
         if self.d_out != (n_q_heads + 2 * n_kv_heads) * head_dim:
             raise ValueError(f"d_out {self.d_out} is not {n_q_heads} + 2 x {n_kv_heads} heads of {head_dim}")
         self.n_q_heads, self.n_kv_heads, self.head_dim, self.max_len = n_q_heads, n_kv_heads, head_dim, max_len
         self.cache = KVCache(self.pool_t, n_pages, page_elems=wl.page_elems, dtype=wl.dtype,
-                             n_kv_heads=n_kv_heads, head_dim=head_dim, tokens_per_page=1)
+                             n_kv_heads=n_kv_heads, head_dim=head_dim, tokens_per_page=tokens_per_page,
+                             bits=kv_bits)
+        self.max_blocks = (max_len + tokens_per_page - 1) // tokens_per_page
         self.rope, self.attention, self.write_options = rope, attention or {}, write or {}
         self.cached: Dict[int, int] = {}  # tokens of each running request in the cache
         self.ws: Optional[torch.Tensor] = None
@@ -563,7 +573,7 @@ class AttentionLoop(ServingLoop):
         """One workspace for every call of the loop, grown as steps need it. calls: (requests,
         prompt tokens) of each, 0 tokens for slora_attn_decode."""
         a = _lib.Attn(n_q_heads=self.n_q_heads)
-        need = max(self.cache.workspace_size(self.cache._kv(r, self.max_len), a, n) for r, n in calls)
+        need = max(self.cache.workspace_size(self.cache._kv(r, self.max_blocks), a, n) for r, n in calls)
         if self.ws is None or self.ws.numel() < need:
             self.ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
         return self.ws
@@ -603,7 +613,7 @@ class AttentionLoop(ServingLoop):
         dev = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(self.device)
         pages = np.concatenate([self.sched.request_pages(r) for r in requests])
         T, S, first = b["n_tokens"], len(prompts), int(b["seg_offsets"][-1])
-        t = KVTables(2, len(requests), self.max_len, T, device=self.device)
+        t = KVTables(2, len(requests), self.max_blocks, T, device=self.device)
         self.cache.tables(t, dev(pages), dev(past), dev(new))
         hq, hk = self.n_q_heads, self.n_kv_heads
         qkv = y.view(TORCH_DTYPES[self.wl.dtype]).view(T, hq + 2 * hk, self.head_dim)

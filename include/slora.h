@@ -279,6 +279,12 @@ typedef struct {
  * (adapters and KV in separate memory). */
 int slora_sched_create(slora_pool* pool, slora_residency* res, const slora_sched_config* cfg,
                        slora_sched** out);
+/* The same with pages that hold tokens_per_page consecutive tokens of a request each (>= 1; 1 is
+ * slora_sched_create): a prompt takes kv_pages_per_token pages for every tokens_per_page tokens
+ * it begins, a running request's next token that many where the pages it has are full, else
+ * none. In the order slora_kv_tables takes pages. */
+int slora_sched_create_paged(slora_pool* pool, slora_residency* res, const slora_sched_config* cfg,
+                             int32_t tokens_per_page, slora_sched** out);
 /* Frees the running requests' KV pages and unpins their adapters, then the scheduler. */
 int slora_sched_destroy(slora_sched* sched);
 /* Queue a request: adapter_id (-1 = none) of rank `rank`, a prompt of prompt_len tokens
@@ -451,8 +457,8 @@ int slora_set_wait_limit(int32_t polls);
  * tokens_per_page * n_kv_heads * head_dim <= page_elems, the rest of the page unused. A
  * "plane" is one layer's K or one layer's V; a request's block b holds its tokens
  * [b * tokens_per_page, (b + 1) * tokens_per_page) and takes one page of every plane.
- * With tokens_per_page = 1 and kv_pages_per_token planes this is what slora_sched
- * allocates.
+ * With kv_pages_per_token planes this is what slora_sched allocates (tokens_per_page = 1, or
+ * that of slora_sched_create_paged).
  *
  * Every length, table and tensor below is in DEVICE memory and read by the kernels only,
  * so the calls need no host copy of them, never block the host, allocate nothing and can
