@@ -59,7 +59,7 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[V], int byte) {
   for (int e = 0; e < V; ++e) {
     t[e] = x[e] * inv;
     t[e] = fmaf(fmaf(-t[e], step, x[e]), inv, t[e]);
-    t[e] = step == 0.f ? 0.f : fminf(fmaxf(t[e], -6.f), 6.f);
+    t[e] = copysignf(fminf(fabsf(t[e]), 6.f), x[e]);  // (also of zeros)
   }
   uint32_t w = 0;
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[0], t[1], 1.0f, 0);
@@ -68,7 +68,7 @@ __device__ __forceinline__ uint32_t codes_of(const float (&x)[V], int byte) {
     w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[4], t[5], 1.0f, 2);
     w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, t[6], t[7], 1.0f, 3);
   }
-  return w;
+  return byte == kNanStep ? 0 : w;
 }
 
 // V, G, INTER as for slora_kv_write.

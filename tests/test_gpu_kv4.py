@@ -13,10 +13,6 @@ from heterogeneous_lora_amd import runtime
 pytestmark = pytest.mark.gpu
 
 
-def rng_of(*parts):
-    return np.random.default_rng([abs(hash(str(p))) % (1 << 30) if isinstance(p, str) else int(p) for p in parts])
-
-
 # ---------------------------------------------------------------- write and read
 
 def written(dtype, hk, hq, d, tpp, n, *, rotary, interleaved=False, norm=False, weights=True, seed=0, pad=0, bend=None):
@@ -64,7 +60,6 @@ def check_bytes(cache, pool, slots, want, lay, tpp):
         cols = torch.from_numpy((at % tpp)[:, None] * size + np.arange(size))
         page = torch.from_numpy(at // tpp)[:, None]
         expect[page, cols] = torch.where(raw < 0, after[page, cols], raw)
-    # a level of zero may carry either sign where the group's step is zero
     assert torch.equal(after, expect), f"{int((after != expect).sum())} bytes differ"
 
 
