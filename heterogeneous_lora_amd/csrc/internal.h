@@ -314,7 +314,7 @@ struct AttnArgs {
   int32_t spans;            // into which all requests' keys are cut
   int2* cut;                // [n_req]: the span a request begins in, the spans it is in
   int32_t* back;            // prefill of 4 bits: tables and K and V in 16 bits, NULL: straight from the codes
-  int32_t xcd_log2;         // 3 where spans go round the XCDs, else 0
+  int32_t xcd_log2;         // 3 where spans or chunks go round the XCDs, else 0
 };
 // Floats of one row's partial result: max, sum, and the head's dimensions.
 inline int64_t attn_part_floats(int32_t D) { return D + 2; }

@@ -507,3 +507,29 @@ def test_2_to_the_30_tokens(op, window, prefix):
         one = SimpleNamespace(hk=1, lens=[len(k)], k=[k], v=[v])
         ref = four.attention(one, q[i:i + 1], [(0, len(k) - 1)], scale=0.3)
         util.check(out[i:i + 1], ref.out, four.bound(ref, "f16", op == "decode"), f"{op} row {i}")
+
+
+@pytest.mark.parametrize("way", ["few", "many", "straight"])
+@pytest.mark.parametrize("hk,group,d", [(1024, 1, 8), (1024, 16, 8), (521, 3, 40), (1, 4096, 64), (63, 5, 136), (17, 17, 256)])
+def test_many_heads(way, hk, group, d):
+    """As many heads as there may be, odd numbers of them, steps that begin anywhere in 16 bytes."""
+    rng = np.random.default_rng(hk + group)
+    lens = [70, 3]
+    c = four.Cache(rng, lens, dtype="bf16", hk=hk, d=d, tpp=1, blocks_more=long_table(hk, 2, 1) if way == "many" else 1)
+    op = "prefill" if way == "straight" else "decode"
+    new = [2, 1] if op == "prefill" else [1, 1]
+    q = torch.from_numpy(rng.standard_normal((sum(new), hk * group, d))).bfloat16()
+    got = call(c, op, q, lens, new=new)
+    ref = four.attention(c, q, rows_of(lens, new), scale=d ** -0.5)
+    back = op == "prefill" and 3 * group >= 2 * 4096
+    util.check(got, ref.out, four.bound(ref, "bf16", op == "decode", back=back), way)
+
+
+@pytest.mark.parametrize("hk,hq,d", [(1024, 2048, 8), (521, 1, 40), (1, 300, 256)])
+def test_write_of_many_heads(hk, hq, d):
+    cache, pool, slots, dev_slots, _, _, want, lay = written("f16", hk, hq, d, 1, 5, rotary=8, norm=True, seed=8)
+    check_bytes(cache, pool, slots, want, lay, 1)
+    k, v = (torch.empty(5, hk, d, dtype=torch.float16, device="cuda") for _ in range(2))
+    cache.read(k, v, *dev_slots)
+    for got, x in ((k, want[0]), (v, want[1])):
+        assert torch.equal(got.cpu().double(), four.values(*four.held(x), d))
