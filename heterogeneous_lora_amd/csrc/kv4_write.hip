@@ -79,6 +79,8 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(Write4 b) {
   const Kv4Layout& lay = b.lay;
   __shared__ double2 angle[kAngles];
   __shared__ uint32_t sm_most[kThreads * 2];  // largest magnitudes of the pieces, by group of lanes
+  __shared__ uint8_t* places[kMaxTok][2];     // of a token's K and V, NULL: none
+  __shared__ int32_t position[kMaxTok];
   const int tid = (int)threadIdx.x;
   const int tok0 = (int)blockIdx.x * a.tpw, n_tok = min(a.tpw, a.n_tok - tok0);
   const int pairs = a.pairs;
@@ -89,6 +91,14 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(Write4 b) {
     double sn, cs;
     sincospi(2.0 * f, &sn, &cs);
     angle[i] = make_double2(cs * a.cs, sn * a.cs);
+  }
+  // (looked up once a token: in the loop below a head would wait for it first)
+  for (int i = tid; i < 2 * n_tok; i += kThreads) {
+    const int64_t tok = tok0 + (i >> 1), slot = a.hk ? (i & 1 ? a.vs : a.ks)[tok] : -1;
+    const int64_t page = (slot >> 32) ? slot / a.tpp : (int64_t)((uint32_t)slot / (uint32_t)a.tpp);
+    places[i >> 1][i & 1] =
+        slot < 0 || page >= a.n_pages ? nullptr : (uint8_t*)(a.pool + page * a.P) + (slot - page * a.tpp) * lay.token_bytes;
+    position[i >> 1] = a.pos[tok];
   }
   __syncthreads();
 
@@ -137,19 +147,14 @@ __global__ __launch_bounds__(kThreads) void kv4_write_kernel(Write4 b) {
   for (int i = tid / G; i < n_tok * n_heads; i += kThreads / G) {
     const int t = i / n_heads, h = h_begin + i - t * n_heads;
     const int64_t tok = tok0 + t;
-    if (a.pos[tok] < 0) continue;
+    if (position[t] < 0) continue;
     const bool is_q = h < a.hq, is_v = h >= a.hq + a.hk;
     const int hh = is_q ? h : is_v ? h - a.hq - a.hk : h - a.hq;
     const uint16_t* src = is_q ? a.q.p + tok * a.q.ts + hh * a.q.hs
                           : is_v ? a.v.p + tok * a.v.ts + hh * a.v.hs
                                  : a.k.p + tok * a.k.ts + hh * a.k.hs;
-    uint8_t* token = nullptr;
-    if (!is_q) {
-      const int64_t slot = (is_v ? a.vs : a.ks)[tok];
-      const int64_t page = (slot >> 32) ? slot / a.tpp : (int64_t)((uint32_t)slot / (uint32_t)a.tpp);
-      if (slot < 0 || page >= a.n_pages) continue;
-      token = (uint8_t*)(a.pool + page * a.P) + (slot - page * a.tpp) * lay.token_bytes;
-    }
+    uint8_t* const token = places[t][is_v];
+    if (!is_q && !token) continue;
     Piece<V> r0{}, r1{};
     if (at.has0) r0 = load<V>(src + at.c0 * V);
     if (at.has1) r1 = load<V>(src + at.c1 * V);

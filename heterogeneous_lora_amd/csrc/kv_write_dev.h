@@ -118,22 +118,19 @@ __device__ __forceinline__ void norm_and_turn(const WriteArgs& a, const Angle* a
     }
   }
   if (INTER) {
+    // (the rotated part ends with a piece)
+    auto turn = [&](int c, F (&z)[V]) {
+      if (c * V / 2 >= a.pairs) return;
 #pragma unroll
-    for (int e = 0; e < V; e += 2) {
-      const int i0 = (at.c0 * V + e) / 2, i1 = (at.c1 * V + e) / 2;
-      if (i0 < a.pairs) {
-        const F c = (F)ang[i0].x, s = (F)ang[i0].y;
-        const F p = x[e], q = x[e + 1];
-        x[e] = p * c - q * s;
-        x[e + 1] = q * c + p * s;
+      for (int e = 0; e < V; e += 2) {
+        const F co = (F)ang[(c * V + e) / 2].x, s = (F)ang[(c * V + e) / 2].y;
+        const F p = z[e], q = z[e + 1];
+        z[e] = p * co - q * s;
+        z[e + 1] = q * co + p * s;
       }
-      if (i1 < a.pairs) {
-        const F c = (F)ang[i1].x, s = (F)ang[i1].y;
-        const F p = y[e], q = y[e + 1];
-        y[e] = p * c - q * s;
-        y[e + 1] = q * c + p * s;
-      }
-    }
+    };
+    turn(at.c0, x);
+    turn(at.c1, y);
   } else if (at.g < at.half) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
