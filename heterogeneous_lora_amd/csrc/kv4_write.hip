@@ -13,10 +13,11 @@
 // is set where something is cut off: step and level are those of the exactly computed value, unless
 // 2^-50 of it decides. (V has no arithmetic before its step, and is exact.)
 //
-// Bound by the vector unit (73% of its cycles, the kernel's beginnings and ends among them), which
-// K keeps busy longest. 16411 tokens of 32 query and 8 + 8 KV heads of 128 with norms: 108 us (131
-// with steps and quotients in 64 bits too; the same with K's heads dealt evenly to the waves of a
-// workgroup). slora_kv_write, which stores four times as much of K and V, takes 91.
+// Bound by the vector unit, which K keeps busy longest (73% of its cycles when it took 108 us). 16411
+// tokens of 32 query and 8 + 8 KV heads of 128 with norms: 96 us (108 with a token's position and
+// slots asked for by each head; 131 with steps and quotients in 64 bits too; one more wave a SIMD
+// spills, 118; 4 or 8 tokens to a workgroup instead of 2, or K's heads dealt evenly to its waves,
+// change nothing). slora_kv_write, which stores four times as much of K and V, takes 91.
 #include "kv_write_dev.h"
 
 namespace slora {
