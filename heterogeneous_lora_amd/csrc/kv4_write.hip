@@ -28,10 +28,11 @@ struct Write4 {
   Kv4Layout lay;
 };
 
-// x cut off to 24 bits, the last of them set if anything was lost (a multiple of 2^-149; an infinity
-// from 2^128 on).
+// x cut off to 24 bits, the last of them set if anything was lost (a multiple of 2^-149; what is
+// finite past the largest float becomes that).
 __device__ __forceinline__ float cut(double x) {
   const float f = (float)x;
+  if (fabs(x) < (double)INFINITY && !(fabsf(f) < INFINITY)) return copysignf(0x1.fffffep127f, f);
   const double lost = fabs(x) - fabs((double)f);
   const int bits = __float_as_int(f);
   return __int_as_float(lost == 0.0 || !(fabsf(f) < INFINITY) ? bits : (lost < 0.0 ? bits - 1 : bits) | 1);
