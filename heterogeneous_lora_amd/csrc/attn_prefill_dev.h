@@ -198,7 +198,8 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
   float slope = MODE >= kBias && a.slopes ? a.slopes[head] * kLog2e : 0.f;
   // Scores are s * mul, or s * mul + cap: with softcap s is the reciprocal 1 / (e^(2 x / cap) +
   // 1) in cap tanh(x / cap) = cap - 2 cap s.
-  const float mul = MODE == kPlain ? (k4 || kScaled ? finite(a.scale2 * q_row) : a.scale2) : MODE == kCap ? -2.0f * a.cap_out : 1.f;
+  // (of a row of zeros a small scale times q_row is 0, which would make NaN of a masked -infinity)
+  const float mul = MODE == kPlain ? (k4 || kScaled ? fmaxf(finite(a.scale2 * q_row), 0x1p-126f) : a.scale2) : MODE == kCap ? -2.0f * a.cap_out : 1.f;
   const float cap_in = k4 || kScaled ? finite(a.cap_in * q_row) : a.cap_in;
 
   f32x16 acc[NC];
