@@ -652,10 +652,14 @@ __global__ __launch_bounds__(W * 64) void attn4_join_kernel(AttnArgs a) {
       __syncthreads();
       if (wave) continue;
     }
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    const float inv = 1.0f / l;
     uint16_t* out = a.out + (int64_t)r * a.o_ts + (int64_t)hq * a.o_hs;
-    if (lane * 2 < a.D) *reinterpret_cast<uint32_t*>(out + lane * 2) = round2<DT>(o1.x * inv, o1.y * inv);
-    if (lane * 2 + 128 < a.D) *reinterpret_cast<uint32_t*>(out + lane * 2 + 128) = round2<DT>(o2.x * inv, o2.y * inv);
+    // (a row with scores of minus infinity alone is 0, also where a V is no number)
+    auto put = [&](int d, float2 o) {
+      if (d < a.D) *reinterpret_cast<uint32_t*>(out + d) = l == 0.f ? 0u : round2<DT>(o.x * inv, o.y * inv);
+    };
+    put(lane * 2, o1);
+    put(lane * 2 + 128, o2);
     if (a.lse && lane == 0) a.lse[(int64_t)r * heads_q + hq] = log_sum<SLORA_F16>(mt, l);
   }
 }
