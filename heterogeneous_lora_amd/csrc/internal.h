@@ -392,11 +392,14 @@ struct Prefill4 {
 constexpr int32_t kBackTokens = 64;                    // of a block
 constexpr int64_t kBackBytes = int64_t(1) << 30;       // at most
 inline Prefill4 prefill4_plan(int32_t n_req, int64_t n_tok, int32_t group, int32_t hk, int32_t D, int32_t max_len) {
-  Prefill4 p;
+  Prefill4 p = {};
   p.blocks = (max_len + kBackTokens - 1) / kBackTokens;
-  p.table_bytes = ((int64_t)n_req * p.blocks * 8 + 255) / 256 * 256;
-  p.bytes = (int64_t)n_req * p.blocks * kBackTokens * hk * D * 4;
-  p.back = n_tok * group >= (int64_t)n_req * (D > 128 ? 32 * D : 4096) && p.bytes > 0 && p.bytes <= kBackBytes;
+  // (by division: all blocks' bytes may pass 64 bits)
+  const int64_t blocks = (int64_t)n_req * p.blocks, block = (int64_t)kBackTokens * hk * D * 4;
+  p.back = n_tok * group >= (int64_t)n_req * (D > 128 ? 32 * D : 4096) && blocks > 0 && blocks <= kBackBytes / block;
+  if (!p.back) return p;
+  p.table_bytes = (blocks * 8 + 255) / 256 * 256;
+  p.bytes = blocks * block;
   return p;
 }
 inline int32_t prefill_waves(int64_t n_tok, int32_t group) {

@@ -153,8 +153,9 @@ inline Prefill4 prefill4_of(const slora_kv* kv, const slora_attn* at, int32_t n_
 }
 inline int64_t prefill_workspace(int bits, const slora_kv* kv, const slora_attn* at, int32_t n_tokens) {
   const int64_t rest = prefill_workspace(kv, at, n_tokens);
+  if (bits != 4) return rest;
   const Prefill4 p = prefill4_of(kv, at, n_tokens);
-  return bits == 4 && p.back ? (rest + 255) / 256 * 256 + p.table_bytes + p.bytes : rest;
+  return p.back ? (rest + 255) / 256 * 256 + p.table_bytes + p.bytes : rest;
 }
 
 inline int workspace_size(const char* what, int bits, const slora_kv* kv, const slora_attn* at, int32_t n_tokens,
