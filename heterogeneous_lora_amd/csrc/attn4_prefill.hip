@@ -59,7 +59,7 @@ __global__ __launch_bounds__(kThreads) void attn4_back_kernel(AttnArgs a, Prefil
   const int32_t n = a.seq[r];
   if (n < 0 || n > a.max_len) return;
   const int32_t q0 = min(max(a.q_offsets[r], 0), a.n_tok), n_new = max(min(max(a.q_offsets[r + 1], 0), a.n_tok) - q0, 0);
-  const int32_t lo = a.window ? max(n - n_new - a.window + 1, 0) : 0;
+  const int32_t lo = first_key_seen(n, n_new, a.window);
   const int32_t prefix = a.prefix ? a.prefix[r] : 0;
   const int32_t j0 = b * kBackTokens, j1 = min(j0 + kBackTokens, n);
   if (n_new == 0 || (j1 <= lo && j0 >= prefix)) return;

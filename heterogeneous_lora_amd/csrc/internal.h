@@ -402,6 +402,12 @@ inline Prefill4 prefill4_plan(int32_t n_req, int64_t n_tok, int32_t group, int32
   p.bytes = blocks * block;
   return p;
 }
+// The first key past the prefix that some row of a request sees: n keys, n_new of them new (more than
+// n: the rows before the first key see none past the prefix).
+constexpr int32_t first_key_seen(int32_t n, int32_t n_new, int32_t window) {
+  const int64_t first = (int64_t)n - n_new - window + 1;
+  return window && first > 0 ? (int32_t)first : 0;
+}
 inline int32_t prefill_waves(int64_t n_tok, int32_t group) {
   return n_tok * group >= 128 ? 4 : (int32_t)((n_tok * group + 31) / 32);
 }

@@ -56,6 +56,17 @@ int main() {
               CHECK(bytes >= wide && (n == 0 || bytes <= wide + kBackBytes + kBackBytes / 256 + 512));
               ++g_calls;
             }
+  const int32_t keys[] = {0, 1, 100, 1 << 25, 1 << 30}, news[] = {0, 1, 99, 100, 1 << 25, INT32_MAX - 1, INT32_MAX},
+                windows[] = {0, 1, 70, (1 << 25) - 1, (1 << 30) - 1};
+  for (int32_t n : keys)
+    for (int32_t m : news)
+      for (int32_t w : windows) {
+        const int32_t lo = first_key_seen(n, m, w);
+        CHECK(lo >= 0 && lo <= n);
+        // the first new row is at n - m; a window holds its own position and w - 1 before it
+        const int64_t position = (int64_t)n - m;
+        CHECK(w == 0 ? lo == 0 : position - w + 1 <= 0 ? lo == 0 : lo == position - w + 1);
+      }
   std::printf("%lld sizes; %lld failed checks\n", (long long)g_calls, (long long)g_fail);
   return g_fail ? 1 : 0;
 }
