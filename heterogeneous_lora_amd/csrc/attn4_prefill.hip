@@ -8,12 +8,10 @@
 // the products, 2 instructions for 2 values and 16 bytes of LDS a store. That is done by every row
 // tile again and costs as many vector instructions as the weights do: long prompts 3785 us against
 // 3200 with a cache of 16 bits. Where a key is seen by many row tiles (Prefill4) it is read back to
-// f16 once, into the workspace, and the 16-bit kernel runs over that, its products in f16 for bf16 q
-// too: the weights' rounding is the same on both ways.
+// 16 bits once, into the workspace, and the 16-bit kernel runs over that.
 //
-// Two prompts of 8000 tokens after 7000-8192 cached, 32 query heads on 8 KV heads of 128, bf16: 3.24
-// ms (954 TFLOP/s; with products in bf16, whose weights lose 2^-8, 3.15), 55 us of it the reading
-// back; 64 prompts of 8 to 512 tokens, 32 heads of 128,
+// Two prompts of 8000 tokens after 7000-8192 cached, 32 query heads on 8 KV heads of 128, bf16: 3.07
+// ms (1006 TFLOP/s), 55 us of it the reading back; 64 prompts of 8 to 512 tokens, 32 heads of 128,
 // straight from the codes: 238 us (with every tile's page ids and codes waited for before the next
 // one's are asked for, at a prompt's beginning: 248).
 #include "attn_prefill_dev.h"
@@ -21,8 +19,7 @@
 namespace slora {
 namespace {
 
-// BITS: 4 straight from the codes, 16 over what was read back.
-template <int DT, int MODE, int BITS>
+template <int DT, int MODE>
 hipError_t launch_mode(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev) {
   const int64_t tiles = ((int64_t)a.n_tok * a.group + kTileM - 1) / kTileM + a.n_req + a.chunks;
   if (tiles * a.hk * kThreads >= kMaxThreads) return hipErrorInvalidConfiguration;
@@ -32,26 +29,26 @@ hipError_t launch_mode(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev)
     hipExtLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, ev.start, ev.stop, 0, a);
     return hipGetLastError();
   };
-  return nc <= 2   ? go(attn_prefill_kernel<DT, 2, MODE, BITS, SLORA_F16>)
-         : nc == 3 ? go(attn_prefill_kernel<DT, 3, MODE, BITS, SLORA_F16>)
-         : nc == 4 ? go(attn_prefill_kernel<DT, 4, MODE, BITS, SLORA_F16>)
-         : nc <= 6 ? go(attn_prefill_kernel<DT, 6, MODE, BITS, SLORA_F16>)
-                   : go(attn_prefill_kernel<DT, 8, MODE, BITS, SLORA_F16>);
+  return nc <= 2   ? go(attn_prefill_kernel<DT, 2, MODE, 4>)
+         : nc == 3 ? go(attn_prefill_kernel<DT, 3, MODE, 4>)
+         : nc == 4 ? go(attn_prefill_kernel<DT, 4, MODE, 4>)
+         : nc <= 6 ? go(attn_prefill_kernel<DT, 6, MODE, 4>)
+                   : go(attn_prefill_kernel<DT, 8, MODE, 4>);
 }
 
-template <int DT, int BITS>
+template <int DT>
 hipError_t launch_dt(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev) {
   const bool cap = a.cap_out != 0.f, bias = a.slopes || !(a.scale2 > 0.f);
-  if (a.cap_out > kNearCap * kLog2e) return launch_mode<DT, kWideCap, BITS>(a, s, ev);
-  return bias && cap ? launch_mode<DT, kBiasCap, BITS>(a, s, ev)
-         : bias      ? launch_mode<DT, kBias, BITS>(a, s, ev)
-         : cap       ? launch_mode<DT, kCap, BITS>(a, s, ev)
-                     : launch_mode<DT, kPlain, BITS>(a, s, ev);
+  if (a.cap_out > kNearCap * kLog2e) return launch_mode<DT, kWideCap>(a, s, ev);
+  return bias && cap ? launch_mode<DT, kBiasCap>(a, s, ev)
+         : bias      ? launch_mode<DT, kBias>(a, s, ev)
+         : cap       ? launch_mode<DT, kCap>(a, s, ev)
+                     : launch_mode<DT, kPlain>(a, s, ev);
 }
 
-// K and V of the keys that some row sees, in f16 (exact, and the products' type whatever q's is), as
-// a cache of blocks of kBackTokens tokens: a workgroup a block of K or V, a thread 8 dimensions at
-// a time.
+// K and V of the keys that some row sees, in 16 bits, as a cache of blocks of kBackTokens tokens: a
+// workgroup a block of K or V, a thread 8 dimensions at a time.
+template <int DT>
 __global__ __launch_bounds__(kThreads) void attn4_back_kernel(AttnArgs a, Prefill4 p) {
   const int r = (int)blockIdx.y, v = (int)blockIdx.z, b = (int)blockIdx.x;
   const int32_t id = (v * a.n_req + r) * p.blocks + b;
@@ -71,11 +68,11 @@ __global__ __launch_bounds__(kThreads) void attn4_back_kernel(AttnArgs a, Prefil
     for (int u = (int)threadIdx.x % 64; u < per_token; u += 64) {
       const int head = u / per_head, x = u - head * per_head;
       const Key4 k = key4_addr(a, page, j, head);
-      const uint32_t w = load_codes<8>(k.good ? k.codes + ((x & 3) * a.kv4.groups + (x >> 2)) * 4 : fill_addr<SLORA_F16>(true));
+      const uint32_t w = load_codes<8>(k.good ? k.codes + ((x & 3) * a.kv4.groups + (x >> 2)) * 4 : fill_addr<DT>(true));
       const uint32_t st = k.good ? *(const SLORA_GLOBAL uint8_t*)(k.steps + (x >> 2)) : 255u;
       const float step = (float)__builtin_bit_cast(_Float16, (uint16_t)(st << 7));
       uint32_t o[4];
-      auto two = [&](auto y, int i) { o[i] = pack2<SLORA_F16>((float)y[0] * step, (float)y[1] * step); };
+      auto two = [&](auto y, int i) { o[i] = pack2<DT>((float)y[0] * step, (float)y[1] * step); };
       two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), 0);
       two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1), 1);
       two(__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), 2);
@@ -88,7 +85,10 @@ __global__ __launch_bounds__(kThreads) void attn4_back_kernel(AttnArgs a, Prefil
 hipError_t launch_back(AttnArgs a, int32_t dtype, hipStream_t s, const LaunchEvents& ev) {
   const Prefill4 p = prefill4_plan(a.n_req, a.n_tok, a.group, a.hk, a.D, a.max_len);
   const dim3 grid((unsigned)p.blocks, (unsigned)a.n_req, 2);
-  hipExtLaunchKernelGGL(attn4_back_kernel, grid, dim3(kThreads), 0, s, ev.start, nullptr, 0, a, p);
+  if (dtype == SLORA_F16)
+    hipExtLaunchKernelGGL(attn4_back_kernel<SLORA_F16>, grid, dim3(kThreads), 0, s, ev.start, nullptr, 0, a, p);
+  else
+    hipExtLaunchKernelGGL(attn4_back_kernel<SLORA_BF16>, grid, dim3(kThreads), 0, s, ev.start, nullptr, 0, a, p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   a.pool = (const uint16_t*)((const uint8_t*)a.back + p.table_bytes);
@@ -101,14 +101,14 @@ hipError_t launch_back(AttnArgs a, int32_t dtype, hipStream_t s, const LaunchEve
   a.vt = a.back + a.n_req * p.blocks;
   LaunchEvents rest;
   rest.stop = ev.stop;
-  return dtype == SLORA_F16 ? launch_attn_prefill(a, dtype, s, rest) : launch_dt<SLORA_BF16, 16>(a, s, rest);
+  return launch_attn_prefill(a, dtype, s, rest);
 }
 
 }  // namespace
 
 hipError_t launch_attn4_prefill(const AttnArgs& a, int32_t dtype, hipStream_t s, const LaunchEvents& ev) {
   if (a.back) return launch_back(a, dtype, s, ev);
-  return dtype == SLORA_F16 ? launch_dt<SLORA_F16, 4>(a, s, ev) : launch_dt<SLORA_BF16, 4>(a, s, ev);
+  return dtype == SLORA_F16 ? launch_dt<SLORA_F16>(a, s, ev) : launch_dt<SLORA_BF16>(a, s, ev);
 }
 
 }  // namespace slora

@@ -1,5 +1,5 @@
 // The kernel of attention of prompts' new tokens (attn_prefill.hip: a cache of 16 bits a value;
-// attn4_prefill.hip: of 4, straight from it or read back to f16).
+// attn4_prefill.hip: of 4).
 #pragma once
 
 #include "attn4_dev.h"
@@ -131,13 +131,12 @@ enum Mode { kPlain, kCap, kBias, kBiasCap, kWideCap };
 
 // Two workgroups a CU leave a wave 256 registers: heads up to 192 fit (192: 2.4 ms against 3.8
 // with one workgroup), 256 would spill (9.4 ms against 4.6).
-// DT: the type of q and out. MT: the products' and, of 16 bits, the cache's.
-template <int DT, int NC, int MODE, int BITS, int MT = BITS == 4 ? SLORA_F16 : DT>
+template <int DT, int NC, int MODE, int BITS>
 __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel(AttnArgs a) {
   using S = Shape<NC>;
   constexpr int BN = S::BN, KT = S::KT, CH = S::CH;
   constexpr bool k4 = BITS == 4;
-  constexpr bool kScaled = DT != MT;  // bf16 q in products of f16
+  constexpr int MT = k4 ? SLORA_F16 : DT;  // the products' type
   __shared__ uint4 sm_k[2][S::kUnits];
   __shared__ uint4 sm_v[2][S::kUnits];
   __shared__ uint64_t sm_addr[k4 ? 1 : 2][k4 ? 1 : 2 * BN];
@@ -185,8 +184,8 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
       q[c] = ld16(d < a.D ? qp + d : kAttnFill.zero);
     }
   }
-  float q_row = 1.f;  // what the row is divided by to be in f16
-  if constexpr (kScaled) {
+  float q_row = 1.f;  // of 4 bits, bf16: what the row is divided by to be in f16
+  if constexpr (k4 && DT == SLORA_BF16) {
     float most = 0.f;
 #pragma unroll
     for (int c = 0; c < NC * 2; ++c) most = fmaxf(most, largest_bf16(q[c]));
@@ -199,8 +198,8 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
   // Scores are s * mul, or s * mul + cap: with softcap s is the reciprocal 1 / (e^(2 x / cap) +
   // 1) in cap tanh(x / cap) = cap - 2 cap s.
   // (of a row of zeros a small scale times q_row is 0, which would make NaN of a masked -infinity)
-  const float mul = MODE == kPlain ? (k4 || kScaled ? fmaxf(finite(a.scale2 * q_row), 0x1p-126f) : a.scale2) : MODE == kCap ? -2.0f * a.cap_out : 1.f;
-  const float cap_in = k4 || kScaled ? finite(a.cap_in * q_row) : a.cap_in;
+  const float mul = MODE == kPlain ? (k4 ? fmaxf(finite(a.scale2 * q_row), 0x1p-126f) : a.scale2) : MODE == kCap ? -2.0f * a.cap_out : 1.f;
+  const float cap_in = k4 ? finite(a.cap_in * q_row) : a.cap_in;
 
   f32x16 acc[NC];
 #pragma unroll
@@ -216,7 +215,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
   // changes the accumulators: otherwise the compiler keeps a second set of them, and every
   // tile pays for copies between the two.)
   const int my_key = tid % BN, is_v = tid / BN % 2;
-  const uint64_t zeros = settled(fill_addr<MT>(true)), nans = settled(fill_addr<MT>(false));
+  const uint64_t zeros = settled(fill_addr<DT>(true)), nans = settled(fill_addr<DT>(false));
   const int32_t* table = (is_v ? a.vt : a.kt) + (int64_t)r * a.max_blocks;
   auto index_of = [&](int turn) { return (turn + 2 - is_v) * BN + my_key; };  // V at turn -2: below 0
   auto key_of = [&](int turn) { return keys.key(max(min(index_of(turn), keys.count - 1), 0)); };
@@ -372,7 +371,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
     for (int e = 0; e < 2; ++e) {
       const int i = j % 8 * 2 + e;
       float x = s[kt][i];
-      if (kScaled && MODE >= kBias) x *= q_row;
+      if (k4 && DT == SLORA_BF16 && MODE >= kBias) x *= q_row;
       if (MODE == kCap) x = __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(x * cap_in) + 1.0f);
       else if (MODE == kBiasCap) x = capped_near(a, x);
       else if (MODE == kWideCap) x = capped(a, x);
@@ -461,7 +460,7 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
         top = __builtin_elementwise_max(top, magnitudes(w.z));
         top = __builtin_elementwise_max(top, magnitudes(w.w));
       }
-      if (__any(not_finite<MT>(__builtin_bit_cast(uint32_t, top)) != 0)) sm_flag[t & 3] = 1;
+      if (__any(not_finite<DT>(__builtin_bit_cast(uint32_t, top)) != 0)) sm_flag[t & 3] = 1;
     }
     __syncthreads();  // everyone's share; and everyone is done with the places about to be filled
     if (edge || cleared) sm_flag[(t + 2) & 3] = 0;
@@ -470,10 +469,10 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
 #pragma unroll 1
       for (int u = 0; u < S::kLoads; ++u) {
         uint4 w = vt[tid + u * kThreads];
-        w.x ^= not_finite<MT>(w.x);
-        w.y ^= not_finite<MT>(w.y);
-        w.z ^= not_finite<MT>(w.z);
-        w.w ^= not_finite<MT>(w.w);
+        w.x ^= not_finite<DT>(w.x);
+        w.y ^= not_finite<DT>(w.y);
+        w.z ^= not_finite<DT>(w.z);
+        w.w ^= not_finite<DT>(w.w);
         vt[tid + u * kThreads] = w;
       }
       __syncthreads();
@@ -613,11 +612,11 @@ __global__ __launch_bounds__(kThreads, NC <= 6 ? 2 : 1) void attn_prefill_kernel
         for (int u = 0; u < 4; ++u) {
           const int dim = d * 32 + 8 * u + 4 * h;
           const uint64_t w = *(const __attribute__((address_space(1))) uint64_t*)(dim < a.D ? row + dim * 2 : zeros);
-          const uint32_t x0 = not_finite<MT>((uint32_t)w) & on, x1 = not_finite<MT>((uint32_t)(w >> 32)) & on;
-          acc[d][4 * u] += lo_f32<MT>(x0);
-          acc[d][4 * u + 1] += hi_f32<MT>(x0);
-          acc[d][4 * u + 2] += lo_f32<MT>(x1);
-          acc[d][4 * u + 3] += hi_f32<MT>(x1);
+          const uint32_t x0 = not_finite<DT>((uint32_t)w) & on, x1 = not_finite<DT>((uint32_t)(w >> 32)) & on;
+          acc[d][4 * u] += lo_f32<DT>(x0);
+          acc[d][4 * u + 1] += hi_f32<DT>(x0);
+          acc[d][4 * u + 2] += lo_f32<DT>(x1);
+          acc[d][4 * u + 3] += hi_f32<DT>(x1);
         }
     }
   }

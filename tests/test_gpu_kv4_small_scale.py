@@ -35,7 +35,8 @@ def test_prefill(hk, hq, d, past, new, cap, dtype, scale):
                   window=20, softcap=cap)
     rows = [(r, a + i) for r, (a, b) in enumerate(zip(past, new)) for i in range(b)]
     ref = four.attention(c, q, rows, scale=scale, window=20, cap=cap)
-    util.check(out, ref.out, four.bound(ref, dtype, False), "prefill")
+    back = sum(new) * hq // hk >= 4096 * len(lens)  # (keys read back first)
+    util.check(out, ref.out, four.bound(ref, dtype, False, back=back), "prefill")
 
 
 @pytest.mark.parametrize("scale", SCALES)
