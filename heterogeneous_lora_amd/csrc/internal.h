@@ -383,7 +383,10 @@ inline int32_t prefill_chunks(int64_t n_tok, int32_t group, int32_t hk, int32_t 
 // values of by 32 row tiles and more (64 of heads of 256); blocks of a request then, bytes of the two
 // tables and of K and V. us straight from the codes and read back, 32 query heads on 8 of 128: 1024
 // tokens of 16 requests (4096 rows) 286 and 258, after 16000 cached 357 and 321; 512 of 8 (2048) 61 and
-// 67, 256 after 8192 (1024) 77 and 89; heads of 256 at 4096 rows 189 and 211.
+// 67, 256 after 8192 (1024) 77 and 89; heads of 256 at 4096 rows 189 and 211. The call knows what the
+// tables have room for, not how many keys there are, and K and V read back are part of the workspace: so
+// only where tables have room for kBackKeys keys a row at most, which is 4 times the bytes of q and out.
+// (1024 tokens in a table of 131072 would ask for 512 MiB.)
 struct Prefill4 {
   bool back;
   int32_t blocks;
@@ -391,12 +394,14 @@ struct Prefill4 {
 };
 constexpr int32_t kBackTokens = 64;                    // of a block
 constexpr int64_t kBackBytes = int64_t(1) << 30;       // at most
+constexpr int32_t kBackKeys = 4;                       // for a row, at most
 inline Prefill4 prefill4_plan(int32_t n_req, int64_t n_tok, int32_t group, int32_t hk, int32_t D, int32_t max_len) {
   Prefill4 p = {};
   p.blocks = (max_len + kBackTokens - 1) / kBackTokens;
   // (by division: all blocks' bytes may pass 64 bits)
   const int64_t blocks = (int64_t)n_req * p.blocks, block = (int64_t)kBackTokens * hk * D * 4;
-  p.back = n_tok * group >= (int64_t)n_req * (D > 128 ? 32 * D : 4096) && blocks > 0 && blocks <= kBackBytes / block;
+  p.back = n_tok * group >= (int64_t)n_req * (D > 128 ? 32 * D : 4096) && blocks > 0 &&
+           blocks * kBackTokens <= kBackKeys * n_tok * group && blocks <= kBackBytes / block;
   if (!p.back) return p;
   p.table_bytes = (blocks * 8 + 255) / 256 * 256;
   p.bytes = blocks * block;

@@ -676,9 +676,11 @@ int slora_kv4_read(const slora_kv* kv, const slora_kv_rows* rows, void* stream);
  * weights exp(s - max) are in slora_attn4_decode with f16 q sums of two f16 values (2^-21 of a
  * weight is lost), otherwise rounded to f16 once (2^-11 of a weight; 2^-32 of the largest if that
  * is more). Long prompts are the exception: where a call has 4096 rows a request on average and more
- * (new tokens times the query heads of a KV head; 32 head_dim rows for heads above 128), the keys are
- * read back first, as far as 1 GiB holds them, and slora_attn4_prefill is slora_attn_prefill over
- * them: K, V and weights are of dtype, and bf16 loses 2^-8 of a weight. A page id outside the pool reads as NaN. Workspaces as for slora_attn_*, which may
+ * (new tokens times the query heads of a KV head; 32 head_dim rows for heads above 128) and tables with
+ * room for 4 keys a row at most, the keys are read back into the workspace first (which is up to 4 times
+ * the bytes of q and out larger for it; not where it would be by more than 1 GiB) and
+ * slora_attn4_prefill is slora_attn_prefill over them: K, V and weights are of dtype, and bf16 loses
+ * 2^-8 of a weight. A page id outside the pool reads as NaN. Workspaces as for slora_attn_*, which may
  * share them. */
 int slora_attn4_workspace_size(const slora_kv* kv, const slora_attn* attn, int32_t n_tokens, int64_t* bytes);
 int slora_attn4_decode(const slora_kv* kv, const slora_attn* attn, void* ws, int64_t ws_bytes, void* stream);

@@ -54,6 +54,8 @@ int main() {
               CHECK(slora_attn4_workspace_size(&kv, &at, n, &bytes) == SLORA_OK);
               // (tables of 8 bytes a block beside the blocks of 64 tokens)
               CHECK(bytes >= wide && (n == 0 || bytes <= wide + kBackBytes + kBackBytes / 256 + 512));
+              // (and K and V read back in no more than 4 times the bytes of q and out)
+              CHECK(n == 0 || bytes - wide <= 4 * (4 * (int64_t)n * hq * d) + kBackBytes / 256 + 512);
               ++g_calls;
             }
   const int32_t keys[] = {0, 1, 100, 1 << 25, 1 << 30}, news[] = {0, 1, 99, 100, 1 << 25, INT32_MAX - 1, INT32_MAX},

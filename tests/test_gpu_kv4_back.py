@@ -139,3 +139,23 @@ def test_heads_masks_and_values_not_seen(dtype, d, hk, tpp, past, new, kw):
     print(f"[margin] {worst:.3f}")
     assert bool((out[T:] == 7.0).all()) and bool((lse[T:] == 0).all())
     assert float((lse[:T].cpu().double() - ref.lse).abs().max()) <= float(2 * ref.d.max()) + 1e-5
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 192), ("f16", 128)])
+def test_wide_tables_are_read_straight(dtype, d):
+    """The same prompt in a table with room for more than 4 keys a row: no workspace for them, and the
+    weights' rounding is that of the other way."""
+    c, q, rows, scale, _ = weights_case(dtype, d, "plain")
+    wide = 4 * rows_for(d) // c.tpp + 64
+    cache, _, _ = c.to_gpu()
+    tables = [torch.from_numpy(np.pad(t, ((0, 0), (0, wide - t.shape[1])), constant_values=-1)).cuda() for t in (c.kt, c.vt)]
+    from heterogeneous_lora_amd import _lib
+    a = _lib.Attn(n_q_heads=q.shape[1])
+    of_16_bits = _lib.KV(1 << 20, 1, c.tpp * d, _lib.DTYPES[dtype], 1, d, c.tpp, 1, wide)
+    assert cache.workspace_size(cache._kv(1, wide), a, len(rows)) == _lib.attn_workspace_size(of_16_bits, a, len(rows))
+    out = torch.full_like(q, 7.0, device="cuda")
+    cache.prefill(q.cuda(), out, *tables, torch.tensor(c.lens, dtype=torch.int32, device="cuda"),
+                  torch.tensor([0, len(rows)], dtype=torch.int32, device="cuda"), scale=scale)
+    ref = four.attention(c, q, rows, scale=scale)
+    util.check(out, ref.out, four.bound(ref, dtype, False), "straight")

@@ -27,3 +27,21 @@ def run_driver(tmp_path, name):
 def test_sizes_at_the_limits(tmp_path):
     out = run_driver(tmp_path, "kv4_limits_driver")
     assert out == "1536 sizes; 0 failed checks\n", out
+
+
+def test_a_wide_table_does_not_ask_for_its_keys():
+    """A prompt's workspace over 4 bits beside the one over 16: by q and out, not by the table."""
+    from heterogeneous_lora_amd import _lib
+    a = _lib.Attn(n_q_heads=32)
+    extra = {}
+    for tokens in (1023, 1024, 1025, 16000):
+        for table in (1040, 4096, 16000, 16640, 131072, 262000, 263000, 1 << 20):
+            sizes = []
+            for bits in (16, 4):
+                P = 8 * 128 if bits == 16 else _lib.kv4_token_bytes(8, 128) // 2
+                kv = _lib.KV(1 << 20, 1 << 20, P, _lib.DTYPES["bf16"], 8, 128, 1, 1, table)
+                sizes.append((_lib.attn_workspace_size if bits == 16 else _lib.attn4_workspace_size)(kv, a, tokens))
+            extra[tokens, table] = sizes[1] - sizes[0]
+            assert extra[tokens, table] <= 4 * (2 * tokens * 32 * 128 * 2) + table // 64 * 8 + 1024
+    assert extra[1024, 4096] == 4096 // 64 * 8 + 4096 * 8 * 128 * 4  # read back: both tables, K and V
+    assert extra[1023, 4096] == extra[1024, 131072] == extra[1024, 1 << 20] == 0
