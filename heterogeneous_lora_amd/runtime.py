@@ -564,16 +564,15 @@ class AttentionLoop(ServingLoop):
         self.cache = KVCache(self.pool_t, n_pages, page_elems=wl.page_elems, dtype=wl.dtype,
                              n_kv_heads=n_kv_heads, head_dim=head_dim, tokens_per_page=tokens_per_page,
                              bits=kv_bits)
-        self.max_blocks = (max_len + tokens_per_page - 1) // tokens_per_page
         self.rope, self.attention, self.write_options = rope, attention or {}, write or {}
         self.cached: Dict[int, int] = {}  # tokens of each running request in the cache
         self.ws: Optional[torch.Tensor] = None
 
-    def _workspace(self, calls) -> torch.Tensor:
+    def _workspace(self, calls, max_blocks: int) -> torch.Tensor:
         """One workspace for every call of the loop, grown as steps need it. calls: (requests,
         prompt tokens) of each, 0 tokens for slora_attn_decode."""
         a = _lib.Attn(n_q_heads=self.n_q_heads)
-        need = max(self.cache.workspace_size(self.cache._kv(r, self.max_blocks), a, n) for r, n in calls)
+        need = max(self.cache.workspace_size(self.cache._kv(r, max_blocks), a, n) for r, n in calls)
         if self.ws is None or self.ws.numel() < need:
             self.ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
         return self.ws
@@ -613,14 +612,16 @@ class AttentionLoop(ServingLoop):
         dev = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(self.device)
         pages = np.concatenate([self.sched.request_pages(r) for r in requests])
         T, S, first = b["n_tokens"], len(prompts), int(b["seg_offsets"][-1])
-        t = KVTables(2, len(requests), self.max_blocks, T, device=self.device)
+        # tables as wide as the longest request now: kernels and workspaces go by what they have room for
+        blocks = -(-int((past + new).max()) // self.cache.tokens_per_page)
+        t = KVTables(2, len(requests), blocks, T, device=self.device)
         self.cache.tables(t, dev(pages), dev(past), dev(new))
         hq, hk = self.n_q_heads, self.n_kv_heads
         qkv = y.view(TORCH_DTYPES[self.wl.dtype]).view(T, hq + 2 * hk, self.head_dim)
         q, k, v = qkv.split([hq, hk, hk], dim=1)
         rotated, out = (torch.empty(T, hq, self.head_dim, dtype=qkv.dtype, device=self.device) for _ in range(2))
         self.cache.write(q, k, v, rotated, t.position, t.slots[0], t.slots[1], rope=self.rope, **self.write_options)
-        ws = self._workspace([(S, first), (len(running), 0)])
+        ws = self._workspace([(S, first), (len(running), 0)], blocks)
         if S:
             self.cache.prefill(rotated[:first], out[:first], t.table[0, :S], t.table[1, :S], t.seq_len[:S],
                                t.q_offsets[:S + 1], ws=ws, **self.attention)
