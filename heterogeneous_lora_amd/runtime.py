@@ -553,10 +553,13 @@ class AttentionLoop(ServingLoop):
     def __init__(self, wl, n_pages: int, n_q_heads: int, n_kv_heads: int, head_dim: int, max_len: int,
                  rope: Optional[Rope] = None, attention: Optional[dict] = None, write: Optional[dict] = None,
                  kv_bits: int = 16, tokens_per_page: Optional[int] = None, **kw):
+        if kv_bits not in (4, 16):
+            raise ValueError(f"kv_bits: expected 4 or 16, got {kv_bits}")
+        token = _lib.kv4_token_bytes(n_kv_heads, head_dim) if kv_bits == 4 else 2 * n_kv_heads * head_dim
         if tokens_per_page is None:
-            tokens_per_page = 1
-            if kv_bits == 4:
-                tokens_per_page = max(2 * wl.page_elems // _lib.kv4_token_bytes(n_kv_heads, head_dim), 1)
+            tokens_per_page = 1 if kv_bits == 16 else max(2 * wl.page_elems // token, 1)
+        if tokens_per_page * token > 2 * wl.page_elems:  # (a step would find it, with requests admitted)
+            raise ValueError(f"{tokens_per_page} tokens of {token} bytes do not fit a page of {2 * wl.page_elems}")
         super().__init__(wl, n_pages, kv_pages_per_token=2, tokens_per_page=tokens_per_page, **kw)
         if self.d_out != (n_q_heads + 2 * n_kv_heads) * head_dim:
             raise ValueError(f"d_out {self.d_out} is not {n_q_heads} + 2 x {n_kv_heads} heads of {head_dim}")
