@@ -10,10 +10,10 @@
 // 3200 with a cache of 16 bits. Where a key is seen by many row tiles (Prefill4) it is read back to
 // 16 bits once, into the workspace, and the 16-bit kernel runs over that.
 //
-// Two prompts of 8000 tokens after 7000-8192 cached, 32 query heads on 8 KV heads of 128, bf16: 3.07
-// ms (1006 TFLOP/s), 55 us of it the reading back; 64 prompts of 8 to 512 tokens, 32 heads of 128,
-// straight from the codes: 238 us (with every tile's page ids and codes waited for before the next
-// one's are asked for, at a prompt's beginning: 248).
+// Two prompts of 8000 tokens after 7000-8192 cached, 32 query heads on 8 KV heads of 128, bf16: 3.13
+// ms (988 TFLOP/s; f16 3.24), 41 us of it the reading back; 64 prompts of 8 to 512 tokens, 32 heads of
+// 128, straight from the codes: 238 us (with every tile's page ids and codes waited for before the
+// next one's are asked for, at a prompt's beginning: 248).
 #include "attn_prefill_dev.h"
 
 namespace slora {
@@ -47,10 +47,13 @@ hipError_t launch_dt(const AttnArgs& a, hipStream_t s, const LaunchEvents& ev) {
 }
 
 // K and V of the keys that some row sees, in 16 bits, as a cache of blocks of kBackTokens tokens: a
-// workgroup a block of K or V, a thread 8 dimensions at a time.
+// workgroup a quarter of a block of K or V, a wave a token, a thread 8 dimensions at a time. (A token
+// waits for its page id, then for its codes, and a wave's tokens for each other: one prompt of 1024
+// tokens takes 42 us in all, 54 with a whole block to a workgroup; long prompts 3128 and 3142.)
+constexpr int kBackSplit = 4, kBackPart = kBackTokens / kBackSplit;
 template <int DT>
 __global__ __launch_bounds__(kThreads) void attn4_back_kernel(AttnArgs a, Prefill4 p) {
-  const int r = (int)blockIdx.y, v = (int)blockIdx.z, b = (int)blockIdx.x;
+  const int r = (int)blockIdx.y, v = (int)blockIdx.z, b = (int)blockIdx.x / kBackSplit, part = (int)blockIdx.x % kBackSplit;
   const int32_t id = (v * a.n_req + r) * p.blocks + b;
   if (threadIdx.x == 0) a.back[id] = id;
   const int32_t n = a.seq[r];
@@ -63,7 +66,8 @@ __global__ __launch_bounds__(kThreads) void attn4_back_kernel(AttnArgs a, Prefil
   const int per_head = a.D / 8, per_token = a.hk * per_head;
   uint16_t* const to = (uint16_t*)((uint8_t*)a.back + p.table_bytes) + (int64_t)id * (kBackTokens * a.row);
   const int32_t* const table = (v ? a.vt : a.kt) + (int64_t)r * a.max_blocks;
-  for (int j = j0 + (int)threadIdx.x / 64; j < j1; j += kThreads / 64) {  // a wave a token
+  const int end = min(j0 + (part + 1) * kBackPart, j1);
+  for (int j = j0 + part * kBackPart + (int)threadIdx.x / 64; j < end; j += kThreads / 64) {
     const int32_t page = table[div_tpp(a, (uint32_t)j)];
     for (int u = (int)threadIdx.x % 64; u < per_token; u += 64) {
       const int head = u / per_head, x = u - head * per_head;
@@ -84,7 +88,7 @@ __global__ __launch_bounds__(kThreads) void attn4_back_kernel(AttnArgs a, Prefil
 
 hipError_t launch_back(AttnArgs a, int32_t dtype, hipStream_t s, const LaunchEvents& ev) {
   const Prefill4 p = prefill4_plan(a.n_req, a.n_tok, a.group, a.hk, a.D, a.max_len);
-  const dim3 grid((unsigned)p.blocks, (unsigned)a.n_req, 2);
+  const dim3 grid((unsigned)p.blocks * kBackSplit, (unsigned)a.n_req, 2);
   if (dtype == SLORA_F16)
     hipExtLaunchKernelGGL(attn4_back_kernel<SLORA_F16>, grid, dim3(kThreads), 0, s, ev.start, nullptr, 0, a, p);
   else

@@ -382,11 +382,12 @@ inline int32_t prefill_chunks(int64_t n_tok, int32_t group, int32_t hk, int32_t 
 // Prefill of 4 bits: whether keys are read back to 16 bits first, where each would otherwise be made
 // values of by 32 row tiles and more (64 of heads of 256); blocks of a request then, bytes of the two
 // tables and of K and V. us straight from the codes and read back, 32 query heads on 8 of 128: 1024
-// tokens of 16 requests (4096 rows) 286 and 258, after 16000 cached 357 and 321; 512 of 8 (2048) 61 and
-// 67, 256 after 8192 (1024) 77 and 89; heads of 256 at 4096 rows 189 and 211. The call knows what the
-// tables have room for, not how many keys there are, and K and V read back are part of the workspace: so
-// only where tables have room for kBackKeys keys a row at most, which is 4 times the bytes of q and out.
-// (1024 tokens in a table of 131072 would ask for 512 MiB.)
+// tokens (4096 rows) of one request 38 and 42, of 2 54 and 49, of 16 287 and 244, of one after 3000
+// cached 98 and 90; 512 (2048 rows) of 8 62 and 60, of 16 after 4000 751 and 680; 256 (1024 rows) of 8
+// after 2000 110 and 115; heads of 256, 4096 rows of 8 requests 142 and 135, 8192 of one 138 and 141.
+// The call knows what the tables have room for, not how many keys there are, and K and V read back are
+// part of the workspace: so only where tables have room for kBackKeys keys a row at most, which is 4
+// times the bytes of q and out. (1024 tokens in a table of 131072 would ask for 512 MiB.)
 struct Prefill4 {
   bool back;
   int32_t blocks;
