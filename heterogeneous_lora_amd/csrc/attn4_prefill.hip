@@ -10,8 +10,8 @@
 // 3200 with a cache of 16 bits. Where a key is seen by many row tiles (Prefill4) it is read back to
 // 16 bits once, into the workspace, and the 16-bit kernel runs over that.
 //
-// Two prompts of 8000 tokens after 7000-8192 cached, 32 query heads on 8 KV heads of 128, bf16: 3.13
-// ms (988 TFLOP/s; f16 3.24), 41 us of it the reading back; 64 prompts of 8 to 512 tokens, 32 heads of
+// Two prompts of 8000 tokens after 7000-8192 cached, 32 query heads on 8 KV heads of 128, bf16: 3.05
+// to 3.13 ms (1000 TFLOP/s; f16 3.18), 41 us of it the reading back; 64 prompts of 8 to 512 tokens, 32 heads of
 // 128, straight from the codes: 238 us (with every tile's page ids and codes waited for before the
 // next one's are asked for, at a prompt's beginning: 248).
 #include "attn_prefill_dev.h"

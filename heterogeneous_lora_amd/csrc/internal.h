@@ -345,7 +345,8 @@ struct Decode4 {
 // Vectors of K that requests may have above which spans pay, us with spans and without: 64 requests
 // of up to 4096 keys, 8 heads (2.1 million) 92 and 91; 3 of 131072 (3.1) 119 and 128; 128 of 1024,
 // 32 heads (4.2) 92 and 123; 512 of 2048, 40 heads (42) 687 and 985; 16 of 512, 32 heads (0.3) 25
-// and 12.
+// and 12. (Requests shorter than their tables have room for pay that: 32 of 512 keys, 8 heads, in
+// tables of 131072 22 and 11; 8 of 100 keys 18 and 5.5.)
 constexpr int64_t kDecode4Vectors = 2500000;
 constexpr int32_t kDecode4Spans = 512;  // two workgroups a CU (256: 974 us, 768: 801, 1024: 703)
 inline Decode4 decode4_plan(int32_t n_req, int32_t hk, int32_t group, int32_t head_dim, int32_t max_len, int32_t window) {

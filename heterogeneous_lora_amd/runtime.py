@@ -345,6 +345,8 @@ def _opt(t: Optional[torch.Tensor]):
 class KVCache:
     """The pool's KV pages as the attention operators see them (slora_kv). bits: of a cached value,
     16 (the cache's type) or 4 (slora.h, "KV cache in 4 bits"; dtype is then that of q, k, v and out).
+    In 4 bits the kernels are chosen by what block tables have room for: they need be no wider than the
+    longest request (tables of 131072 tokens for requests of 512: twice the time of a decode).
 
     Each bind_* method checks shapes and types, marshals one call's arguments once and
     returns a no-argument callable; the method of the same name without bind_ makes the call
